@@ -226,6 +226,110 @@ int spear_linear_forward_path(const spear_layer* layer, const uint16_t* x, int M
  * *device_status receives SPEAR_OK or the first device-side error code. */
 int spear_read_status(void* ws, int* device_status, void* stream);
 
+/* ---- key-value cache ---------------------------------------------------------
+ * A paged cache of attention keys and values, beside the layers whose outputs
+ * it holds: bf16, or quantised with the same symmetric round-to-nearest rule
+ * as the weights (spear_w4_quantize), one fp16 scale per token, head and
+ * side.  For a row w of head_dim values and top code Q (127 or 7):
+ *     s = fp16_rne(max|w| / Q)   (fp32 arithmetic; saturated to 65504;
+ *                                 s == 0 becomes 1.0 with all codes 0;
+ *                                 a NaN in the row makes s NaN, codes 0)
+ *     c = clamp(rint_even(w / s), -Q, Q)   (IEEE fp32 quotient)
+ * and the row stands for c * s.  Bit-exact and deterministic. */
+enum { SPEAR_KV_BF16 = 0, SPEAR_KV_INT8 = 1, SPEAR_KV_INT4 = 2 };
+
+typedef struct spear_kv_cache {
+  int kind;       /* SPEAR_KV_*                                                        */
+  int n_pages;    /* n_pages * page_size < 2^31                                        */
+  int page_size;  /* tokens per page: a power of two, 16 to 1024                       */
+  int n_heads;    /* heads of keys and values, 1 to 1024                               */
+  int head_dim;   /* 64, 128 or 256                                                    */
+  void* k;        /* device, [n_pages][n_heads][page_size][head_dim]: bf16; int8 codes */
+  void* v;        /*   (two's complement); or int4 codes, byte j of a row holding      */
+                  /*   (c[2j] + 8) | (c[2j+1] + 8) << 4                                */
+  uint16_t* k_scales; /* device fp16, [n_pages][n_heads][page_size] (NULL for bf16)    */
+  uint16_t* v_scales;
+  /* Distance of consecutive pages, for pages that lie inside a larger
+   * allocation (K and V of a page side by side, pages of several layers):
+   * bytes for k and v, elements for the scales.  Multiples of 16 bytes, at
+   * least a page; 0 = pages lie back to back. */
+  long long page_stride;
+  long long scale_stride;
+} spear_kv_cache;
+
+/* Bytes of one page of k (or v), and scales of one page (0 for bf16, or for a
+ * kind, page_size, n_heads or head_dim outside the list above). */
+size_t spear_kv_page_bytes(int kind, int page_size, int n_heads, int head_dim);
+size_t spear_kv_page_scales(int kind, int page_size, int n_heads, int head_dim);
+
+/* Write n new tokens.  A token's slot is page * page_size + offset in the page.
+ * k, v    device bf16, n rows of n_heads * head_dim; ld_k, ld_v: elements
+ *         between consecutive rows (a multiple of 8; at least a row), so that
+ *         column ranges of one projection's output can be passed as they are.
+ * slots   device int32 [n].  A negative slot skips its token (padding).  The
+ *         others must differ from one another: a slot given twice in a call
+ *         ends with an unspecified mixture of its tokens.
+ * ws      device, 256 bytes or more, as of spear_workspace_init: a slot past
+ *         the cache's end is skipped and reported there as
+ *         SPEAR_ERR_DEVICE_CHECK (spear_read_status).
+ * n >= 0 (0: nothing is launched). */
+int spear_kv_write(const spear_kv_cache* cache, const uint16_t* k, long long ld_k, const uint16_t* v, long long ld_v,
+                   const int* slots, int n, void* ws, size_t ws_bytes, void* stream);
+
+/* Read n tokens back: k_out, v_out device bf16 [n][n_heads][head_dim] (dense),
+ * bf16_rne(c * s).  Slots may repeat; a negative slot's rows are zeros, and so
+ * are those of a slot past the cache's end, which is reported as above. */
+int spear_kv_read(const spear_kv_cache* cache, const int* slots, int n, uint16_t* k_out, uint16_t* v_out, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/* ---- attention of one new token per sequence over the cache --------------------
+ * For sequence b, query head h (kv head h / (n_q_heads / n_heads)) and its
+ * seq_lens[b] cached tokens t (the new token's own among them, once written):
+ *     s_t = scale * q . k_t,   p = softmax(s),   out = sum_t p_t v_t,
+ *     lse = log(sum_t exp(s_t)).
+ * A sequence without tokens has out = 0 and lse = -inf.
+ * q, out     device bf16, n_seqs rows of n_q_heads * head_dim; ld_q, ld_out:
+ *            elements between rows (multiples of 8, at least a row).  They must
+ *            not overlap.
+ * n_q_heads  a multiple of the cache's n_heads, at most 1024.
+ * page_table device int32, n_seqs rows of max_pages entries, ld_table apart:
+ *            token t of sequence b lies in page page_table[b][t / page_size].
+ *            Entries past a sequence's length are not read.
+ * seq_lens   device int32 [n_seqs], each 0 to max_pages * page_size.
+ * lse        optional (NULL): device fp32 [n_seqs][n_q_heads].
+ * ws         device workspace of ws_bytes >= spear_attn_workspace_bytes,
+ *            initialised once by spear_workspace_init, of its own: not one
+ *            that layer calls use, and not shared by two calls that may run
+ *            concurrently.
+ * A length outside its range is cut to it and a page number outside the cache
+ * leaves its tokens' keys and values zero; both are reported as
+ * SPEAR_ERR_DEVICE_CHECK (spear_read_status), and the sequence's results are
+ * then unspecified.  0 <= n_seqs <= 4096 (0: nothing is launched).  The result does not depend on
+ * timing: the split over the cache is a function of the lengths alone. */
+size_t spear_attn_workspace_bytes(const spear_kv_cache* cache, int n_q_heads);
+int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q, long long ld_q, int n_seqs, int n_q_heads,
+                      const int* page_table, int max_pages, int ld_table, const int* seq_lens, float scale,
+                      uint16_t* out, long long ld_out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- norms around a block, with its gate and residual scale --------------------
+ * What lies between two blocks of a decoder: the residual update after one
+ * (its output y optionally normalised and gated), and the norm before the
+ * next.  Per row, in fp32, x_out and h each rounded once:
+ *     u = y * rsqrt(mean(y^2) + eps) * post_weight    (post_weight NULL: u = y)
+ *     x_out = residual_scale * x + block_scale * gate * u      (gate NULL: 1)
+ *     h = x_out * rsqrt(mean(x_out^2) + eps) * pre_weight (pre_weight NULL: 1)
+ * h is taken from the fp32 sum, before its rounding to x_out.
+ * x, y, x_out, h  device bf16 M x K, dense.  y NULL: no residual update
+ *            (x_out must be NULL, residual_scale is not applied, h = norm(x)).
+ *            x_out or h may be NULL, not both.  Each may be x or y (in place);
+ *            any other overlap of an output is refused.
+ * gate       device bf16: rows of K elements, gate_ld apart; gate_ld 0 = one
+ *            row for all tokens, otherwise a multiple of 8, at least K.
+ * Shapes: K a multiple of 8, 8 to 16384; 0 <= M <= 2^20 (0: nothing is launched). */
+int spear_block_norm(const uint16_t* x, const uint16_t* y, int M, int K, const uint16_t* post_weight,
+                     const uint16_t* gate, long long gate_ld, float residual_scale, float block_scale,
+                     const uint16_t* pre_weight, float eps, uint16_t* x_out, uint16_t* h, void* stream);
+
 /* ---- failure injection (tests of the device-side error path only) -----------
  * Makes one bounded device wait impossible to satisfy in the launches that
  * follow, until called again with kernel 0: the wait expects a publication

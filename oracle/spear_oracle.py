@@ -405,3 +405,68 @@ def ec_pack(A_bits: np.ndarray, B_bits: np.ndarray, w_g_bits: np.ndarray,
     else:
         BpT = np.asarray(B_bits, dtype=np.uint16).T
     return np.ascontiguousarray(AgT), np.ascontiguousarray(BpT)
+
+
+# ---------------------------------------------------------------------------
+# the decoder step around the layer: key-value cache, attention, norms
+# ---------------------------------------------------------------------------
+KV_TOP = {"int8": 127, "int4": 7}
+
+
+def kv_quantize(x, kind):
+    """Codes (int8) and fp16 scales of rows (last axis) of bf16 values given as
+    float64: s = fp16(max|w| / Q), c = clamp(rint(fp32(w / s)), -Q, Q)."""
+    top = np.float32(KV_TOP[kind])
+    x = np.asarray(x, dtype=np.float32)
+    with np.errstate(all="ignore"):
+        s = (np.max(np.abs(x), axis=-1) / top).astype(np.float32)   # np.max keeps NaN
+        s = np.where(s > 65504.0, np.float32(65504.0), s).astype(np.float16)
+        zero = s == 0
+        s = np.where(zero, np.float16(1.0), s)
+        q = np.rint((x / s.astype(np.float32)[..., None]).astype(np.float32))
+        q = np.clip(q, -top, top)
+    q = np.where(zero[..., None] | np.isnan(s)[..., None], 0.0, q)
+    return q.astype(np.int8), s
+
+
+def kv_pack4(q):
+    """int4 codes -> bytes, two per byte, even index in the low half, offset by 8."""
+    u = (q.astype(np.int16) + 8).astype(np.uint8)
+    return u[..., 0::2] | (u[..., 1::2] << 4)
+
+
+def kv_values(q, s):
+    """float64 values of codes and scales."""
+    return q.astype(np.float64) * s.astype(np.float64)[..., None]
+
+
+def attend(q, k, v, scale):
+    """One query row per head over its keys and values: q H x D, k, v L x G x D
+    (head h reads h // (H / G)); float64.  Returns out H x D, lse H and the
+    weights p H x L."""
+    H, D = q.shape
+    L, G, _ = k.shape
+    out, lse, ps = np.zeros((H, D)), np.full(H, -np.inf), np.zeros((H, L))
+    for h in range(H):
+        if L == 0:
+            continue
+        s = scale * (k[:, h // (H // G)] @ q[h])
+        top = s.max()
+        e = np.exp(s - top)
+        ps[h] = e / e.sum()
+        out[h] = ps[h] @ v[:, h // (H // G)]
+        lse[h] = top + np.log(e.sum())
+    return out, lse, ps
+
+
+def block_norm(x, y, post, gate, a, b, pre, eps):
+    """float64 x_out and h of the norms around a block (None where absent)."""
+    if y is not None:
+        u = y
+        if post is not None:
+            u = u / np.sqrt(np.mean(u * u, axis=-1, keepdims=True) + eps) * post
+        if gate is not None:
+            u = u * gate
+        x = a * x + b * u
+    h = x / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + eps)
+    return x, (h if pre is None else h * pre)

@@ -21,8 +21,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspear.so")
 LIB_CHECKED = os.path.join(PKG, "libspear_checked.so")
-SOURCES = ["api.cu", "pack.cu", "decode.cu", "decode2.cu", "decode3.cu", "ec.cu", "tc_gemm.cu", "noalloc.cu"]
-HEADERS = ["common.cuh", "kernels.h", "tma.cuh"]
+SOURCES = ["api.cu", "pack.cu", "decode.cu", "decode2.cu", "decode3.cu", "ec.cu", "tc_gemm.cu", "noalloc.cu",
+           "kv_cache.cu", "attn_decode.cu", "block_norm.cu"]
+HEADERS = ["common.cuh", "kernels.h", "tma.cuh", "kv_cache.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -31,6 +31,8 @@ int set_error(int code, const char* fmt, ...) {
   return code;
 }
 
+void clear_error() { g_last_error.clear(); }
+
 int set_cuda_error(const char* what, cudaError_t e) {
   return set_error(SPEAR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }

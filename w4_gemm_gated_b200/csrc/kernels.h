@@ -15,6 +15,8 @@ struct WsHeader;
 int set_cuda_error(const char* what, cudaError_t e);
 // Record a message as the thread's last error; returns `code`.
 int set_error(int code, const char* fmt, ...);
+// Forget the thread's last error (at the start of a call).
+void clear_error();
 
 // Failure injection for tests (spear_test_inject_timeout): the kernel whose
 // publication wait is made unsatisfiable (0 none, 1 decode, 2 tensor core),

@@ -1,0 +1,44 @@
+// The paged key-value cache as the kernels see it (spear_kv_cache, validated).
+#pragma once
+
+#include <initializer_list>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace spear {
+
+struct KvView {
+  int kind, n_pages, log_page, page_size, heads, dim;
+  uint8_t* k;
+  uint8_t* v;
+  __half* ks;
+  __half* vs;
+  long long page_stride, scale_stride;  // bytes, elements
+};
+
+// Bits of a stored value.
+__host__ __device__ constexpr int kv_bits(int kind) {
+  return kind == SPEAR_KV_BF16 ? 16 : kind == SPEAR_KV_INT8 ? 8 : 4;
+}
+
+// Validate a public cache description; SPEAR_OK or the status to return.
+int check_kv_cache(const spear_kv_cache* c, KvView* out);
+
+inline bool ptr_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// f(kind, dim) as a compile-time pair.
+template <class F>
+void for_kind_dim(int kind, int dim, F f) {
+  auto with_dim = [&](auto kc) {
+    if (dim == 64) f(kc, std::integral_constant<int, 64>{});
+    if (dim == 128) f(kc, std::integral_constant<int, 128>{});
+    if (dim == 256) f(kc, std::integral_constant<int, 256>{});
+  };
+  if (kind == SPEAR_KV_BF16) with_dim(std::integral_constant<int, SPEAR_KV_BF16>{});
+  if (kind == SPEAR_KV_INT8) with_dim(std::integral_constant<int, SPEAR_KV_INT8>{});
+  if (kind == SPEAR_KV_INT4) with_dim(std::integral_constant<int, SPEAR_KV_INT4>{});
+}
+
+}  // namespace spear

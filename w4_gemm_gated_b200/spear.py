@@ -38,12 +38,16 @@ PATH_UNFUSED = 3
 PATH_SEMIFUSED = 4
 GATE_SCALAR = 0
 GATE_RANK_MLP = 1
+KV_BF16 = 0
+KV_INT8 = 1
+KV_INT4 = 2
 PATH_NAMES = {PATH_DECODE: "decode", PATH_FUSED: "fused", PATH_UNFUSED: "unfused", PATH_SEMIFUSED: "semifused"}
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _f = ctypes.c_float
+_ll = ctypes.c_longlong
 
 
 class LayerStruct(ctypes.Structure):
@@ -57,6 +61,16 @@ class LayerStruct(ctypes.Structure):
         ("gate_w1", _vp), ("gate_b1", _vp), ("gate_w2", _vp), ("gate_b2", _vp),
         ("gate_alpha", _f),
         ("prefetch_next", _vp),
+    ]
+
+
+class KVCacheStruct(ctypes.Structure):
+    """Mirror of ``spear_kv_cache``."""
+
+    _fields_ = [
+        ("kind", _i), ("n_pages", _i), ("page_size", _i), ("n_heads", _i), ("head_dim", _i),
+        ("k", _vp), ("v", _vp), ("k_scales", _vp), ("v_scales", _vp),
+        ("page_stride", ctypes.c_longlong), ("scale_stride", ctypes.c_longlong),
     ]
 
 
@@ -87,6 +101,14 @@ EXPORTS = {
     "spear_read_status": (_i, _vp, ctypes.POINTER(_i), _vp),
     "spear_linear_forward_decode_noalloc": (_i, ctypes.POINTER(LayerStruct), _vp, _i, _vp, _vp, _vp, _vp),
     "spear_read_status_noalloc": (_i, ctypes.POINTER(_i), _vp),
+    "spear_kv_page_bytes": (_sz, _i, _i, _i, _i),
+    "spear_kv_page_scales": (_sz, _i, _i, _i, _i),
+    "spear_kv_write": (_i, ctypes.POINTER(KVCacheStruct), _vp, _ll, _vp, _ll, _vp, _i, _vp, _sz, _vp),
+    "spear_kv_read": (_i, ctypes.POINTER(KVCacheStruct), _vp, _i, _vp, _vp, _vp, _sz, _vp),
+    "spear_attn_workspace_bytes": (_sz, ctypes.POINTER(KVCacheStruct), _i),
+    "spear_attn_decode": (_i, ctypes.POINTER(KVCacheStruct), _vp, _ll, _i, _i, _vp, _i, _i, _vp, _f, _vp, _ll, _vp,
+                          _vp, _sz, _vp),
+    "spear_block_norm": (_i, _vp, _vp, _i, _i, _vp, _vp, _ll, _f, _f, _vp, _f, _vp, _vp, _vp),
     "spear_test_inject_timeout": (_i, _i, ctypes.c_longlong),
     "spear_device_checks_enabled": (_i,),
     "spear_set_tracing": (_i, _i),
@@ -315,6 +337,268 @@ def read_status(ws: torch.Tensor, stream=None) -> int:
     v = _i(0)
     _check(F["spear_read_status"](_ptr(ws), ctypes.byref(v), _stream(stream)))
     return v.value
+
+
+# --------------------------------------------------------------------------
+# the decoder step around the layers: key-value cache, attention, norms
+# --------------------------------------------------------------------------
+
+_KV_DTYPES = {torch.bfloat16: KV_BF16, torch.int8: KV_INT8, torch.uint8: KV_INT4}
+
+
+@dataclass
+class KVCache:
+    """Paged key-value cache on the device (keeps its tensors alive; the
+    layouts are ``spear_kv_cache``'s).  Make it with :func:`make_kv_cache` or
+    :func:`kv_cache_from_parts`."""
+
+    kind: int
+    n_pages: int
+    page_size: int
+    n_heads: int
+    head_dim: int
+    k: torch.Tensor                        # n_pages x n_heads x page_size x head_dim (int4: head_dim / 2 bytes)
+    v: torch.Tensor
+    k_scales: torch.Tensor | None = None   # n_pages x n_heads x page_size fp16 (None for bf16)
+    v_scales: torch.Tensor | None = None
+
+    def __post_init__(self):
+        quant = self.kind != KV_BF16
+        self.device = self.k.device
+        self.struct = KVCacheStruct(
+            self.kind, self.n_pages, self.page_size, self.n_heads, self.head_dim, self.k.data_ptr(), self.v.data_ptr(),
+            self.k_scales.data_ptr() if quant else None, self.v_scales.data_ptr() if quant else None,
+            self.k.stride(0) * self.k.element_size() if self.n_pages > 1 else 0,
+            self.k_scales.stride(0) if quant and self.n_pages > 1 else 0)
+        self._ref = ctypes.byref(self.struct)
+
+
+def _dense_pages(t: torch.Tensor) -> bool:
+    """Contiguous but for the distance between pages."""
+    return t[0].is_contiguous() and (t.shape[0] == 1 or t.stride(0) >= t[0].numel())
+
+
+def kv_cache_from_parts(k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor | None = None,
+                        v_scales: torch.Tensor | None = None) -> KVCache:
+    """A cache over existing device tensors: k, v n_pages x n_heads x page_size x
+    head_dim (bf16, int8, or uint8 with two int4 codes per byte), scales
+    n_pages x n_heads x page_size fp16 for the quantised kinds.  Pages may lie
+    apart (views into a larger allocation), k and v alike."""
+    kind = _KV_DTYPES.get(k.dtype)
+    if kind is None or v.dtype != k.dtype:
+        raise TypeError("k and v must both be bf16, int8 or uint8 (int4 pairs)")
+    if k.dim() != 4 or v.shape != k.shape or k.shape[0] < 1:
+        raise ValueError("k and v must be n_pages x n_heads x page_size x head_dim, of one shape")
+    n_pages, n_heads, page_size, width = k.shape
+    tensors = [k, v]
+    if kind == KV_BF16:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("a bf16 cache has no scales")
+    else:
+        if k_scales is None or v_scales is None:
+            raise ValueError("a quantised cache needs k_scales and v_scales")
+        for t in (k_scales, v_scales):
+            if t.dtype != torch.float16 or t.shape != k.shape[:3]:
+                raise ValueError("scales must be fp16, n_pages x n_heads x page_size")
+        tensors += [k_scales, v_scales]
+    for t in tensors:
+        if not t.is_cuda or t.device != k.device:
+            raise ValueError("cache tensors must live on one CUDA device")
+        if not _dense_pages(t):
+            raise ValueError("every page must be contiguous, and pages must not overlap")
+    if n_pages > 1 and (v.stride(0) != k.stride(0) or (kind != KV_BF16 and v_scales.stride(0) != k_scales.stride(0))):
+        raise ValueError("k and v (and their scales) must have the same distance between pages")
+    head_dim = 2 * width if kind == KV_INT4 else width
+    if F["spear_kv_page_bytes"](kind, page_size, n_heads, head_dim) == 0:
+        raise SpearError(ERR_UNSUPPORTED_SHAPE, f"bad cache kind={kind} page_size={page_size} n_heads={n_heads} "
+                                                f"head_dim={head_dim}")
+    return KVCache(kind, n_pages, page_size, n_heads, head_dim, k, v, k_scales, v_scales)
+
+
+def make_kv_cache(kind: int, n_pages: int, page_size: int, n_heads: int, head_dim: int, device=None) -> KVCache:
+    """A zeroed cache of kind KV_BF16, KV_INT8 or KV_INT4."""
+    if F["spear_kv_page_bytes"](kind, page_size, n_heads, head_dim) == 0 or n_pages < 1:
+        raise SpearError(ERR_UNSUPPORTED_SHAPE, f"bad cache kind={kind} n_pages={n_pages} page_size={page_size} "
+                                                f"n_heads={n_heads} head_dim={head_dim}")
+    dtype = {KV_BF16: torch.bfloat16, KV_INT8: torch.int8, KV_INT4: torch.uint8}[kind]
+    shape = (n_pages, n_heads, page_size)
+    width = head_dim // 2 if kind == KV_INT4 else head_dim
+    device = device or torch.device("cuda")
+    k, v = (torch.zeros((*shape, width), dtype=dtype, device=device) for _ in range(2))
+    ks = vs = None
+    if kind != KV_BF16:
+        ks, vs = (torch.zeros(shape, dtype=torch.float16, device=device) for _ in range(2))
+    return kv_cache_from_parts(k, v, ks, vs)
+
+
+def _call(device: torch.device, stream, tensors, fn) -> None:
+    """fn(raw stream) on `device`, whichever device is current: on its current
+    stream, or on `stream`, whose use of the tensors the allocator is told."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    if device.index == torch.cuda.current_device():
+        _check(fn(stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream))
+        return
+    with torch.cuda.device(device):
+        _check(fn(stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream))
+
+
+def _on(device: torch.device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors must live on one CUDA device: got {t.device} beside {device}")
+
+
+def _rows(t: torch.Tensor, n_heads: int, head_dim: int, what: str) -> int:
+    """Elements between the rows of n_heads x head_dim bf16 values of t (2-D or 3-D)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be bf16")
+    row = n_heads * head_dim
+    if t.dim() == 3:
+        ok = t.shape[1:] == (n_heads, head_dim) and t.stride(2) == 1 and (n_heads == 1 or t.stride(1) == head_dim)
+    else:
+        ok = t.dim() == 2 and t.shape[1] == row and t.stride(1) == 1
+    if not ok:
+        raise ValueError(f"{what} must have rows of {n_heads} x {head_dim} consecutive values")
+    return t.stride(0) if t.shape[0] > 1 else row
+
+
+def _i32(t: torch.Tensor, n: int, what: str) -> None:
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be {n} contiguous int32 values")
+
+
+def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, ws: torch.Tensor,
+             stream=None) -> None:
+    """Write n new tokens' keys and values (n x n_heads x head_dim or n x (n_heads
+    * head_dim) bf16; rows may be ranges of wider rows) at their slots (int32,
+    page * page_size + offset; negative: skipped; no slot twice)."""
+    n = k.shape[0]
+    ld_k, ld_v = (_rows(t, cache.n_heads, cache.head_dim, w) for t, w in ((k, "k"), (v, "v")))
+    if v.shape[0] != n:
+        raise ValueError("k and v must have one row per slot")
+    _i32(slots, n, "slots")
+    _on(cache.device, k, v, slots, ws)
+    kp, vp, sp, wp, wn = k.data_ptr(), v.data_ptr(), slots.data_ptr(), _ptr(ws), ws.numel() * ws.element_size()
+    _call(cache.device, stream, (k, v, slots, ws, cache.k, cache.v, cache.k_scales, cache.v_scales),
+          lambda st: F["spear_kv_write"](cache._ref, kp, ld_k, vp, ld_v, sp, n, wp, wn, st))
+
+
+def kv_read(cache: KVCache, slots: torch.Tensor, ws: torch.Tensor, k_out: torch.Tensor | None = None,
+            v_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The keys and values at n slots, n x n_heads x head_dim bf16 (a negative slot reads as zeros)."""
+    n = slots.shape[0]
+    _i32(slots, n, "slots")
+    shape = (n, cache.n_heads, cache.head_dim)
+    k_out, v_out = _outputs(cache.device, stream, shape, k_out, v_out)
+    for t in (k_out, v_out):
+        if t.dtype != torch.bfloat16 or t.numel() != n * cache.n_heads * cache.head_dim:
+            raise ValueError(f"k_out and v_out must be bf16 of shape {shape}")
+    _on(cache.device, slots, ws, k_out, v_out)
+    kp, vp, sp, wp, wn = _ptr(k_out), _ptr(v_out), slots.data_ptr(), _ptr(ws), ws.numel() * ws.element_size()
+    _call(cache.device, stream, (slots, ws, k_out, v_out, cache.k, cache.v, cache.k_scales, cache.v_scales),
+          lambda st: F["spear_kv_read"](cache._ref, sp, n, kp, vp, wp, wn, st))
+    return k_out, v_out
+
+
+def _outputs(device, stream, shape, *given):
+    """The given bf16 outputs, with the missing ones allocated on the stream that writes them."""
+    if all(t is not None for t in given):
+        return given
+    if stream is None:
+        return tuple(torch.empty(shape, dtype=torch.bfloat16, device=device) if t is None else t for t in given)
+    with torch.cuda.stream(stream):
+        return _outputs(device, None, shape, *given)
+
+
+def attn_workspace_bytes(cache: KVCache, n_q_heads: int) -> int:
+    n = F["spear_attn_workspace_bytes"](cache._ref, n_q_heads)
+    if n == 0:
+        raise SpearError(ERR_UNSUPPORTED_SHAPE, f"n_q_heads={n_q_heads} over a cache of {cache.n_heads} heads")
+    return n
+
+
+def make_attn_workspace(cache: KVCache, n_q_heads: int, stream=None) -> torch.Tensor:
+    """A workspace for attn_decode (any batch), kv_write and kv_read on this cache or others of its shape."""
+    n = attn_workspace_bytes(cache, n_q_heads)
+    ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    _call(cache.device, stream, (ws,), lambda st: F["spear_workspace_init"](ws.data_ptr(), n, st))
+    return ws
+
+
+def attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, ws: torch.Tensor,
+                scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence over its cached tokens.
+    q: n_seqs x n_q_heads x head_dim or n_seqs x (n_q_heads * head_dim) bf16,
+    rows may be ranges of wider rows; page_table: n_seqs x max_pages int32;
+    seq_lens: int32; scale: 1 / sqrt(head_dim) if None; lse: optional fp32
+    n_seqs x n_q_heads, written.  Returns out, of q's shape."""
+    n = q.shape[0]
+    D = cache.head_dim
+    H = q.shape[1] if q.dim() == 3 else q.shape[1] // D
+    ld_q = _rows(q, H, D, "q")
+    if out is None:
+        out, = _outputs(cache.device, stream, q.shape, None)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ld_out = _rows(out, H, D, "out")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n \
+            or page_table.stride(1) != 1 and page_table.shape[1] > 1:
+        raise ValueError("page_table must be n_seqs x max_pages int32 with consecutive rows")
+    _i32(seq_lens, n, "seq_lens")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, H) or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32, n_seqs x n_q_heads")
+    _on(cache.device, q, out, page_table, seq_lens, lse, ws)
+    pages = page_table.shape[1]
+    ld_table = page_table.stride(0) if n > 1 else pages
+    args = (q.data_ptr(), ld_q, n, H, page_table.data_ptr(), pages, ld_table, seq_lens.data_ptr(),
+            D ** -0.5 if scale is None else scale, out.data_ptr(), ld_out,
+            None if lse is None else lse.data_ptr(), _ptr(ws), ws.numel() * ws.element_size())
+    _call(cache.device, stream, (q, out, page_table, seq_lens, lse, ws, cache.k, cache.v, cache.k_scales,
+                                 cache.v_scales), lambda st: F["spear_attn_decode"](cache._ref, *args, st))
+    return out
+
+
+def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, pre_weight: torch.Tensor | None = None,
+               post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+               residual_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6,
+               x_out: torch.Tensor | None = None, h: torch.Tensor | None = None, norm: bool = True,
+               stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """The residual update after a block and the norm before the next:
+    x_out = residual_scale x + block_scale gate norm(y; post_weight),
+    h = norm(x_out; pre_weight); with no post_weight y is taken as it is, with
+    no y h = norm(x).  x, y: M x K bf16; weights K; gate K, 1 x K or M x K bf16 (rows
+    may lie apart).  Returns (x_out, h), (x, h) without y; x_out=x updates x in place."""
+    if x.dim() != 2:
+        raise ValueError("x must be M x K")
+    M, K = x.shape
+    for t, what, shape in ((x, "x", (M, K)), (y, "y", (M, K)), (x_out, "x_out", (M, K)), (h, "h", (M, K)),
+                           (pre_weight, "pre_weight", (K,)), (post_weight, "post_weight", (K,))):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape != shape):
+            raise ValueError(f"{what} must be bf16 of shape {shape}")
+    gate_ld = 0
+    if gate is not None:
+        rows = gate.view(1, K) if gate.dim() == 1 and gate.shape[0] == K else gate
+        if rows.dtype != torch.bfloat16 or rows.dim() != 2 or rows.shape[1] != K or rows.shape[0] not in (1, M) \
+                or rows.stride(1) != 1 and K > 1:
+            raise ValueError("gate must be bf16, K, 1 x K or M x K, with consecutive rows")
+        gate_ld = rows.stride(0) if rows.shape[0] > 1 else 0
+    if y is not None:
+        if x_out is None:
+            x_out, = _outputs(x.device, stream, (M, K), None)
+    if not norm:
+        h = None
+    elif h is None:
+        h, = _outputs(x.device, stream, (M, K), None)
+    _on(x.device, y, pre_weight, post_weight, gate, x_out, h)
+    args = (_ptr(x), _ptr(y), M, K, _ptr(post_weight), None if gate is None else gate.data_ptr(), gate_ld,
+            residual_scale, block_scale, _ptr(pre_weight), eps, _ptr(x_out), _ptr(h))
+    _call(x.device, stream, (x, y, pre_weight, post_weight, gate, x_out, h),
+          lambda st: F["spear_block_norm"](*args, st))
+    return (x if y is None else x_out), h
 
 
 def test_inject_timeout(kernel: int, wait_cycles: int = 0) -> None:
