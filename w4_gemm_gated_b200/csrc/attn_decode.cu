@@ -1,8 +1,38 @@
 // Attention of one new token per sequence over the paged cache.
 //
-// One CTA per (query head, sequence); its warps take tokens in turn, each lane
-// holding head_dim / 32 values, with a running maximum and sum of the softmax
-// per warp, joined in shared memory at the end.
+//   out_h = sum_t p_t v_t,  p = softmax(scale q_h . k_t)
+//
+// Bound by HBM: each cached byte is read once and used for the few query heads
+// that share it (two operations per value and head).
+//
+// Work.  A unit is one (sequence, kv head) with up to 8 NT query heads; its
+// tokens are cut into tiles of TILE.  All units' tiles in order form one line,
+// which is cut into equal runs, one per warp, by the lengths alone (every CTA
+// sums them up): ragged batches load the machine evenly, a long sequence is
+// spread over many warps, and a warp takes many short ones without meeting
+// anybody.  A warp streams its run through its own ring of shared-memory
+// stages (16-byte asynchronous copies, rows past a sequence's end filled with
+// zeros), so that copies cross the units' borders and never wait for another
+// warp.
+//
+// Arithmetic.  Tensor-core products over 16 tokens with the query heads as the 8
+// columns: S = K q (rows: tokens), then O^T += V^T P with P's layout turned by
+// movmatrix.  Running maximum, sum and output of a softmax in fp32, in powers of
+// two; the output is rescaled only when a maximum grows.  The weight times
+// its value's scale is rounded to bf16 as the operand of the second product
+// (relative 2^-8 per weight, of the size of the output's own rounding); the sum
+// in the denominator is of the unrounded weights.  int8 codes become bf16
+// exactly, as (128 + low 7 bits) - (128 or 256 by the sign); int4 codes enter as
+// 128 + u, u = c + 8, exact, and 136 times the sum of the other operand is
+// taken off in fp32.
+//
+// Joining.  A warp whose run starts or ends inside a unit leaves (maximum, sum,
+// output) in shared memory; the CTA joins the pieces of a unit in order, and
+// a unit that crosses CTAs is joined, again in order, by whichever of them
+// arrives last (a counter per unit, left at zero): no launch waits, and the
+// result does not depend on who is last.
+#include <atomic>
+
 #include "kv_cache.cuh"
 
 namespace spear {
@@ -15,95 +45,730 @@ struct AttnArgs {
   const int* table;
   const int* lens;
   long long ld_q, ld_out;
-  int ld_table, max_pages, n_seqs, heads, group;
-  float scale;
+  int ld_table, max_len, n_seqs, heads, group;
+  int blocks;   // units per kv head: ceil(group / (8 NT))
+  int stages;   // ring stages per warp
+  int piece;    // floats of a piece: heads of a unit x (DIM + 2)
+  float scale;  // times log2(e)
   WsHeader* hdr;
+  int* tickets;  // one per CTA: arrivals at the unit that first crosses out of it
+  float* parts;  // two pieces per CTA
 };
 
-template <int KIND, int E>
-__device__ __forceinline__ void load_row(const uint8_t* p, float s, int lane, float (&f)[E]) {
-  if constexpr (KIND == SPEAR_KV_BF16) {
-    const __nv_bfloat16* r = reinterpret_cast<const __nv_bfloat16*>(p) + lane * E;
-#pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = __bfloat162float(r[i]);
-  } else if constexpr (KIND == SPEAR_KV_INT8) {
-    const int8_t* r = reinterpret_cast<const int8_t*>(p) + lane * E;
-#pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = s * (float)r[i];
-  } else {
-    const uint8_t* r = p + lane * E / 2;
-#pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = s * (float)((int)((r[i / 2] >> (4 * (i & 1))) & 0xF) - 8);
+constexpr int kMinTiles = 2;  // tiles a warp should have before more warps take part
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most n of this thread's copy groups are in flight.
+__device__ __forceinline__ void cp_wait(int n) {
+  if (n <= 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else asm volatile("cp.async.wait_group 4;" ::: "memory");
+}
+constexpr int kMaxStages = 6;
+
+template <int N>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+  if constexpr (N == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ float lds_half(uint32_t addr) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ float exp2_(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(a), "r"(m), "r"(o));  // (a & m) | o
+  return v;
+}
+// int8 codes in bytes 0 and 2 -> the two codes as bf16, exactly: two's
+// complement is the low 7 bits minus 128 times the top one.
+__device__ __forceinline__ uint32_t int8x2(uint32_t w) {
+  const uint32_t low = and_or(w, 0x007F007Fu, 0x43004300u);  // 128 + low 7 bits
+  const uint32_t top = and_or(w, 0x00800080u, 0x43004300u);  // 128 or 256
+  const __nv_bfloat162 d =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&low), *reinterpret_cast<const __nv_bfloat162*>(&top));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+// 4-bit codes in bits 0-3 and 16-19 -> 128 + u as bf16, exactly.
+__device__ __forceinline__ uint32_t int4x2(uint32_t w) { return and_or(w, 0x000F000Fu, 0x43004300u); }
+constexpr float kInt4Offset = 136.f;  // 128 + 8
+
+// Layout of a unit's tiles in shared memory and in the fragments.
+template <int KIND, int DIM>
+struct Lay {
+  static constexpr int RB = DIM * kv_bits(KIND) / 8;       // bytes of a row
+  static constexpr int TS = RB >= 128 ? 1 : 2;             // blocks of 16 tokens per tile
+  static constexpr int TILE = 16 * TS;
+  static constexpr bool QUANT = KIND != SPEAR_KV_BF16;
+  static constexpr int SIDE = TILE * RB;                   // K (or V) bytes of a stage
+  static constexpr int STAGE = 2 * SIDE + (QUANT ? 4 * TILE : 0);
+  // dims of a lane's run in O: dim = (a / (VL / 2)) 8 VL + rho VL + 2 (a % (VL / 2)) + {0, 1}
+  static constexpr int VL = KIND == SPEAR_KV_BF16 ? 8 : KIND == SPEAR_KV_INT8 ? (DIM >= 128 ? 16 : 8) : DIM / 8;
+  static constexpr int VW = VL * kv_bits(KIND) / 32;       // 32-bit words of such a run
+  static constexpr int KW = DIM * kv_bits(KIND) / 128 >= 4 ? 4 : DIM * kv_bits(KIND) / 128;  // words per K load
+  static constexpr int KI = DIM * kv_bits(KIND) / 128 / KW;                                 // K loads per row
+
+  // Row r of a fragment's 16 is token tok(r) of the block, and the 16-byte
+  // chunks of a row are permuted by xk / xv, so that the 8 rows x 4 lanes of a
+  // K load and the 4 tokens x 8 lanes of a V load each meet all banks.
+  static __device__ __forceinline__ int tok(int r) {
+    if constexpr (RB >= 128) return r;
+    const int c = (r >> 1) & 3;
+    return (r & 8) + ((r & 1) ? 4 + (RB == 64 ? c ^ 1 : (c + 2) & 3) : c);
   }
+  static __device__ __forceinline__ int xk(int t) { return RB >= 128 ? (t & 1) << 2 : RB == 64 ? t & 2 : 0; }
+  static __device__ __forceinline__ int xv(int t) { return RB >= 128 ? ((t >> 1) & 3) << 1 : RB == 64 ? t & 2 : 0; }
+};
+
+__device__ __forceinline__ int clamp_len(const AttnArgs& p, int b) {
+  const int n = __ldg(p.lens + b);
+  return n < 0 ? 0 : min(n, p.max_len);
 }
 
-template <int KIND, int DIM>
-__global__ void __launch_bounds__(256) attn_kernel(AttnArgs p) {
-  constexpr int E = DIM / 32;
-  __shared__ float sm_m[8], sm_l[8], sm_acc[8][DIM];
-  const int head = blockIdx.x, b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int kvh = head / p.group;
-  int len = p.lens[b];
-  const long long most = (long long)p.max_pages << p.c.log_page;
-  if (len < 0 || len > most) {
-    if (threadIdx.x == 0) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
-    len = len < 0 ? 0 : (int)most;
+// A place on the line of tiles.
+struct Place {
+  int b, u, j, nt, len;
+};
+
+template <int TILE>
+__device__ __forceinline__ void advance(const AttnArgs& p, int units, Place& c) {
+  if (++c.j < c.nt) return;
+  c.j = 0;
+  if (++c.u < units) return;
+  c.u = 0;
+  do {
+    if (++c.b >= p.n_seqs) return;
+    c.len = clamp_len(p, c.b);
+    c.nt = (c.len + TILE - 1) / TILE;
+  } while (c.nt == 0);
+}
+
+// A warp's unfinished part of a unit.
+struct Piece {
+  long long start;  // the unit's first tile on the line
+  int nt;           // its tiles
+  int unit;         // b * units + u; -1: no piece
+  int from, to;     // tiles [from, to)
+};
+
+struct Split {
+  long long q;  // tiles per worker, the first `more` of them one more
+  int more;
+  __device__ __forceinline__ long long begin(int w) const { return q * w + min(w, more); }
+  __device__ __forceinline__ int owner(long long t) const {
+    const long long border = (q + 1) * more;
+    return t < border ? (int)(t / (q + 1)) : more + (int)((t - border) / q);
   }
-  float q[E], acc[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = __bfloat162float(p.q[b * p.ld_q + head * DIM + lane * E + i]) * p.scale;
-    acc[i] = 0.f;
-  }
-  for (int t = warp; t < len; t += 8) {
-    const int page = p.table[(long long)b * p.ld_table + (t >> p.c.log_page)];
-    float k[E], v[E];
-    if ((unsigned)page < (unsigned)p.c.n_pages) {
-      const long long prow = (long long)kvh * p.c.page_size + (t & (p.c.page_size - 1));
-      const long long at = page * p.c.page_stride + prow * (DIM * kv_bits(KIND) / 8);
-      float ks = 1.f, vs = 1.f;
-      if constexpr (KIND != SPEAR_KV_BF16) {
-        ks = __half2float(p.c.ks[page * p.c.scale_stride + prow]);
-        vs = __half2float(p.c.vs[page * p.c.scale_stride + prow]);
+};
+
+template <int KIND, int DIM, int NT, int W, int PER_SM>
+__global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_constant__ AttnArgs p) {
+  using L = Lay<KIND, DIM>;
+  constexpr int TILE = L::TILE, TS = L::TS, RB = L::RB, MT = DIM / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long scan_warp[W], line;
+  __shared__ Piece pieces[2 * W];  // a warp's first (unit begun before it), its last
+  __shared__ int order[2 * W];
+  __shared__ int joins[2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rho = lane >> 2, cl = lane & 3;
+  const int units = p.c.heads * p.blocks;
+
+  // ---- the line: tiles before each sequence --------------------------------------
+  long long* before = reinterpret_cast<long long*>(smem);  // n_seqs + 1 of them, in the rings' place
+  const int per = (p.n_seqs + W * 32 - 1) / (W * 32);
+  {
+    long long sum = 0;
+    const int b0 = tid * per, b1 = min(b0 + per, p.n_seqs);
+    for (int b = b0; b < b1; ++b) {
+      if (blockIdx.x == 0) {
+        const int n = __ldg(p.lens + b);
+        if (n < 0 || n > p.max_len) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
       }
-      load_row<KIND, E>(p.c.k + at, ks, lane, k);
-      load_row<KIND, E>(p.c.v + at, vs, lane, v);
-    } else {
-      if (lane == 0) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
-#pragma unroll
-      for (int i = 0; i < E; ++i) k[i] = v[i] = 0.f;
+      sum += (clamp_len(p, b) + TILE - 1) / TILE;
     }
-    float s = 0.f;
+    long long inc = sum;
 #pragma unroll
-    for (int i = 0; i < E; ++i) s = fmaf(q[i], k[i], s);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    const float m1 = fmaxf(m, s), a = m == -INFINITY ? 0.f : expf(m - m1), e = expf(s - m1);
-    m = m1;
-    l = l * a + e;
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = acc[i] * a + e * v[i];
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    if (lane == 31) scan_warp[warp] = inc;
+    __syncthreads();
+    long long off = inc - sum;
+    for (int w = 0; w < warp; ++w) off += scan_warp[w];
+    for (int b = b0; b < b1; ++b) {
+      before[b] = off;
+      off += (clamp_len(p, b) + TILE - 1) / TILE;
+    }
+    if (tid == W * 32 - 1) before[p.n_seqs] = line = off;
+    __syncthreads();
   }
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
+  const long long total = line * units;
+  // sequences without tokens
+  for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x)
+    if (before[b] == before[b + 1]) {
+      for (int i = tid; i < p.heads * DIM / 8; i += W * 32)
+        *reinterpret_cast<uint4*>(p.out + b * p.ld_out + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (int h = tid; h < p.heads; h += W * 32) p.lse[(long long)b * p.heads + h] = -INFINITY;
+    }
+  // ---- this warp's run -------------------------------------------------------------
+  const int workers = (int)min((long long)gridDim.x * W, (total + kMinTiles - 1) / kMinTiles);
+  if ((int)blockIdx.x * W >= workers) return;  // nothing for the whole CTA
+  Split split;
+  split.q = total / workers;
+  split.more = (int)(total - split.q * workers);
+  const int worker = blockIdx.x * W + warp;
+  const long long t0 = worker < workers ? split.begin(worker) : 0;
+  const int n = worker < workers ? (int)(split.begin(worker + 1) - t0) : 0;
+  Place in = {};  // next tile to copy
+  if (n > 0) {
+    int lo = 0, hi = p.n_seqs;  // before[lo] * units <= t0 < before[hi] * units
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] * units <= t0) lo = mid;
+      else hi = mid;
+    }
+    in.b = lo;
+    in.len = clamp_len(p, lo);
+    in.nt = (in.len + TILE - 1) / TILE;
+    const long long r = t0 - before[lo] * units;
+    in.u = (int)(r / in.nt);
+    in.j = (int)(r - (long long)in.u * in.nt);
   }
+  Place at = in;  // tile to work on
+  if (lane == 0) pieces[2 * warp].unit = pieces[2 * warp + 1].unit = -1;
+  __syncthreads();  // the rings take over `before`'s place
+
+  const int ring_bytes = p.stages * L::STAGE;
+  uint8_t* ring = smem + (size_t)warp * (ring_bytes + p.piece * 4);
+  float* first_piece = reinterpret_cast<float*>(ring + ring_bytes);
+  float* last_piece = reinterpret_cast<float*>(ring);  // once the run is through
+  const uint32_t ring_a = smem_u32(ring);
+
+  int page[TS];  // pages of the next tile to copy
+  auto load_pages = [&](const Place& c) {
+    const int* row = p.table + (long long)c.b * p.ld_table;
 #pragma unroll
-  for (int i = 0; i < E; ++i) sm_acc[warp][lane * E + i] = acc[i];
-  __syncthreads();
-  float top = -INFINITY;
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, sm_m[w]);
-  for (int d = threadIdx.x; d < DIM; d += 256) {
-    float total = 0.f, o = 0.f;
-    for (int w = 0; w < 8; ++w)
-      if (sm_m[w] != -INFINITY) {
-        const float e = expf(sm_m[w] - top);
-        total += e * sm_l[w];
-        o += e * sm_acc[w][d];
+    for (int s = 0; s < TS; ++s) {
+      const int t = c.j * TILE + 16 * s;
+      page[s] = t < c.len ? __ldg(row + (t >> p.c.log_page)) : 0;
+    }
+  };
+  auto copy_tile = [&](uint32_t stage) {
+    const int head = in.u / p.blocks;
+#pragma unroll
+    for (int s = 0; s < TS; ++s) {
+      const int t = in.j * TILE + 16 * s, rows = in.len - t;
+      if (rows > 0) {
+        const bool ok = (unsigned)page[s] < (unsigned)p.c.n_pages;
+        if (!ok && lane == 0) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
+        const long long pg = ok ? page[s] : 0;
+        const long long prow = (long long)head * p.c.page_size + (t & (p.c.page_size - 1));
+        const uint8_t* ks = p.c.k + pg * p.c.page_stride + prow * RB;
+        const uint8_t* vs = p.c.v + pg * p.c.page_stride + prow * RB;
+#pragma unroll
+        for (int i = 0; i < RB / 32; ++i) {
+          const int id = i * 32 + lane, row = id / (RB / 16), ch = id % (RB / 16);
+          const int bytes = ok && row < rows ? 16 : 0;
+          const uint32_t d = stage + (16 * s + row) * RB;
+          cp_async16(d + ((ch ^ L::xk(row)) << 4), ks + id * 16, bytes);
+          cp_async16(d + L::SIDE + ((ch ^ L::xv(row)) << 4), vs + id * 16, bytes);
+        }
+        if constexpr (L::QUANT) {
+          if (lane < 4) {  // 16 scales of K, 16 of V
+            const __half* src = (lane & 2 ? p.c.vs : p.c.ks) + pg * p.c.scale_stride + prow + (lane & 1) * 8;
+            cp_async16(stage + 2 * L::SIDE + (lane & 2) * TILE + 32 * s + (lane & 1) * 16, src, ok ? 16 : 0);
+          }
+        }
       }
-    p.out[b * p.ld_out + head * DIM + d] = __float2bfloat16_rn(len ? o / total : 0.f);
-    if (d == 0 && p.lse) p.lse[(long long)b * p.heads + head] = len ? top + logf(total) : -INFINITY;
+    }
+  };
+
+  // ---- the run ------------------------------------------------------------------------
+  float acc[MT][NT][4], m[NT][2], l[NT][2];
+  float psum[NT][4];        // int4: sums of the rounded weights
+  float kfix[NT][2];        // int4: -136 sum of q
+  uint32_t qf[NT][DIM / 8];
+  int from = 0;             // first tile of the current piece
+  int done = 0;             // copies issued
+  if (n > 0) load_pages(in);
+  auto issue = [&]() {
+    if (done < n) {
+      copy_tile(ring_a + (done % p.stages) * L::STAGE);
+      advance<TILE>(p, units, in);
+      if (done + 1 < n) load_pages(in);
+    }
+    ++done;
+    cp_commit();
+  };
+  for (int i = 0; i < p.stages - 1; ++i) issue();
+  for (int i = 0; i < n; ++i) {
+    cp_wait(p.stages - 2);
+    __syncwarp();  // tile i is in, and every lane is through with tile i - 1
+    issue();
+    const uint32_t st = ring_a + (i % p.stages) * L::STAGE;
+    const int head = at.u / p.blocks, blk = at.u - head * p.blocks;
+    const int h0 = head * p.group + blk * 8 * NT, gn = min(8 * NT, p.group - blk * 8 * NT);
+    if (i == 0 || at.j == 0) {
+      // a new piece: the unit's query heads as B fragments, columns past them zero
+      from = at.j;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[a][nt][e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) psum[nt][e] = 0.f;
+        const bool live = nt * 8 + rho < gn;
+        const __nv_bfloat16* qr = p.q + at.b * p.ld_q + (long long)(h0 + nt * 8 + rho) * DIM;
+        constexpr int QB = KIND == SPEAR_KV_BF16 ? 8 : KIND == SPEAR_KV_INT8 ? 16 : (DIM >= 128 ? 32 : 16);
+        // lane c holds dims [4 QB i + QB c, + QB) for each i
+#pragma unroll
+        for (int i8 = 0; i8 < DIM / 32; ++i8) {
+          const int d = (i8 / (QB / 8)) * 4 * QB + QB * cl + (i8 % (QB / 8)) * 8;
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (live) w = __ldg(reinterpret_cast<const uint4*>(qr + d));
+          uint32_t* f = qf[nt] + 4 * i8;
+          if constexpr (KIND == SPEAR_KV_BF16) {
+            f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
+          } else if constexpr (KIND == SPEAR_KV_INT8) {  // bytes 0, 2 and 1, 3 of a word
+            f[0] = __byte_perm(w.x, w.y, 0x5410), f[1] = __byte_perm(w.x, w.y, 0x7632);
+            f[2] = __byte_perm(w.z, w.w, 0x5410), f[3] = __byte_perm(w.z, w.w, 0x7632);
+          } else {  // nibbles i and i + 4 of a word
+            f[0] = __byte_perm(w.x, w.z, 0x5410), f[1] = __byte_perm(w.x, w.z, 0x7632);
+            f[2] = __byte_perm(w.y, w.w, 0x5410), f[3] = __byte_perm(w.y, w.w, 0x7632);
+          }
+        }
+        if constexpr (KIND == SPEAR_KV_INT4) {
+          const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+          float sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < DIM / 8; k += 2) mma_bf16_16816(sq, ones, qf[nt][k], qf[nt][k + 1]);
+          kfix[nt][0] = -kInt4Offset * sq[0];
+          kfix[nt][1] = -kInt4Offset * sq[1];
+        }
+      }
+    }
+    // ---- scores: S[token][head] ---------------------------------------------------------
+    const int rows = at.len - at.j * TILE;  // live tokens from the tile's first on
+    float s[TS][NT][4];
+    float top[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < TS; ++b) {
+      if (16 * b < rows) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[b][nt][e] = KIND == SPEAR_KV_INT4 ? kfix[nt][e & 1] : 0.f;
+        const int r0 = L::tok(rho), r1 = L::tok(rho + 8);
+        const uint32_t ka = st + (16 * b + r0) * RB, kb = st + (16 * b + r1) * RB;
+#pragma unroll
+        for (int i4 = 0; i4 < L::KI; ++i4) {
+          uint32_t x[L::KW], y[L::KW];
+          if constexpr (L::KW == 4) {
+            lds(ka + (((4 * i4 + cl) ^ L::xk(r0)) << 4), x);
+            lds(kb + (((4 * i4 + cl) ^ L::xk(r1)) << 4), y);
+          } else {
+            lds(ka + cl * 4 * L::KW, x);
+            lds(kb + cl * 4 * L::KW, y);
+          }
+          if constexpr (KIND == SPEAR_KV_BF16) {
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const uint32_t a[4] = {x[k], y[k], x[k + 1], y[k + 1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[b][nt], a, qf[nt][4 * i4 + k], qf[nt][4 * i4 + k + 1]);
+            }
+          } else if constexpr (KIND == SPEAR_KV_INT8) {
+#pragma unroll
+            for (int k = 0; k < L::KW; ++k) {
+              const uint32_t a[4] = {int8x2(x[k]), int8x2(y[k]), int8x2(x[k] >> 8), int8x2(y[k] >> 8)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_bf16_16816(s[b][nt], a, qf[nt][2 * (L::KW * i4 + k)], qf[nt][2 * (L::KW * i4 + k) + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < L::KW; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a[4] = {int4x2(x[k] >> (8 * h)), int4x2(y[k] >> (8 * h)), int4x2(x[k] >> (8 * h + 4)),
+                                       int4x2(y[k] >> (8 * h + 4))};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_bf16_16816(s[b][nt], a, qf[nt][4 * (L::KW * i4 + k) + 2 * h],
+                                 qf[nt][4 * (L::KW * i4 + k) + 2 * h + 1]);
+              }
+          }
+        }
+        float f0 = p.scale, f1 = p.scale;
+        if constexpr (L::QUANT) {
+          const uint32_t sa = st + 2 * L::SIDE + 32 * b;
+          f0 *= lds_half(sa + 2 * r0);
+          f1 *= lds_half(sa + 2 * r1);
+        }
+        const bool ok0 = 16 * b + r0 < rows, ok1 = 16 * b + r1 < rows;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[b][nt][e] = ok0 ? s[b][nt][e] * f0 : -INFINITY;
+            s[b][nt][e + 2] = ok1 ? s[b][nt][e + 2] * f1 : -INFINITY;
+            top[nt][e] = fmaxf(top[nt][e], fmaxf(s[b][nt][e], s[b][nt][e + 2]));
+          }
+      }
+    }
+    // ---- running maximum; what is there is scaled down where it grew -----------------------
+    bool grew = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xFFFFFFFFu, top[nt][e], d));
+        top[nt][e] = fmaxf(top[nt][e], m[nt][e]);
+        grew |= top[nt][e] > m[nt][e];
+      }
+    if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          f[e] = m[nt][e] == -INFINITY ? 0.f : exp2_(m[nt][e] - top[nt][e]);
+          m[nt][e] = top[nt][e];
+          l[nt][e] *= f[e];
+        }
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[a][nt][e] *= f[e & 1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) psum[nt][e] *= f[e & 1];
+      }
+    }
+    // ---- weights, and O^T += V^T P -----------------------------------------------------------
+#pragma unroll
+    for (int b = 0; b < TS; ++b) {
+      if (16 * b < rows) {
+        const int r0 = L::tok(rho), r1 = L::tok(rho + 8);
+        const bool ok0 = 16 * b + r0 < rows, ok1 = 16 * b + r1 < rows;
+        float f0 = 1.f, f1 = 1.f;
+        if constexpr (L::QUANT) {
+          // scales of rows past the end may be anything
+          const uint32_t sa = st + 2 * L::SIDE + 2 * TILE + 32 * b;
+          f0 = ok0 ? lds_half(sa + 2 * r0) : 0.f;
+          f1 = ok1 ? lds_half(sa + 2 * r1) : 0.f;
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float e[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e[k] = exp2_(s[b][nt][k] - m[nt][k & 1]);
+          l[nt][0] += e[0] + e[2];
+          l[nt][1] += e[1] + e[3];
+          pb[nt][0] = movmatrix(pack_bf16x2(e[0] * f0, e[1] * f0));
+          pb[nt][1] = movmatrix(pack_bf16x2(e[2] * f1, e[3] * f1));
+          if constexpr (KIND == SPEAR_KV_INT4) {
+            const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+            mma_bf16_16816(psum[nt], ones, pb[nt][0], pb[nt][1]);
+          }
+        }
+        const uint32_t va = st + L::SIDE + 16 * b * RB;
+        const int tk[4] = {L::tok(2 * cl), L::tok(2 * cl + 1), L::tok(2 * cl + 8), L::tok(2 * cl + 9)};
+#pragma unroll
+        for (int blk8 = 0; blk8 < DIM / (8 * L::VL); ++blk8) {
+          uint32_t v[4][L::VW];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (L::VW == 4) {
+              lds(va + tk[k] * RB + (((8 * blk8 + rho) ^ L::xv(tk[k])) << 4), v[k]);
+            } else if constexpr (L::VW == 2) {
+              lds(va + tk[k] * RB + (((rho >> 1) ^ L::xv(tk[k])) << 4) + (rho & 1) * 8, v[k]);
+            } else {
+              lds(va + tk[k] * RB + rho * 4, v[k]);
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < L::VW; ++w) {
+            // the same values of two tokens side by side: low halves, high halves
+            const uint32_t lo01 = __byte_perm(v[0][w], v[1][w], 0x5410), hi01 = __byte_perm(v[0][w], v[1][w], 0x7632);
+            const uint32_t lo89 = __byte_perm(v[2][w], v[3][w], 0x5410), hi89 = __byte_perm(v[2][w], v[3][w], 0x7632);
+            constexpr int PER = L::VL / 2 / L::VW;  // products per word: 1, 2 or 4
+            const int a0 = blk8 * (L::VL / 2) + w * PER;
+            if constexpr (KIND == SPEAR_KV_BF16) {
+              const uint32_t a[4] = {lo01, hi01, lo89, hi89};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
+            } else if constexpr (KIND == SPEAR_KV_INT8) {
+              const uint32_t a[4] = {int8x2(lo01), int8x2(lo01 >> 8), int8x2(lo89), int8x2(lo89 >> 8)};
+              const uint32_t c[4] = {int8x2(hi01), int8x2(hi01 >> 8), int8x2(hi89), int8x2(hi89 >> 8)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_bf16_16816(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
+                mma_bf16_16816(acc[a0 + 1][nt], c, pb[nt][0], pb[nt][1]);
+              }
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a[4] = {int4x2(lo01 >> (8 * h)), int4x2(lo01 >> (8 * h + 4)), int4x2(lo89 >> (8 * h)),
+                                       int4x2(lo89 >> (8 * h + 4))};
+                const uint32_t c[4] = {int4x2(hi01 >> (8 * h)), int4x2(hi01 >> (8 * h + 4)), int4x2(hi89 >> (8 * h)),
+                                       int4x2(hi89 >> (8 * h + 4))};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma_bf16_16816(acc[a0 + h][nt], a, pb[nt][0], pb[nt][1]);
+                  mma_bf16_16816(acc[a0 + 2 + h][nt], c, pb[nt][0], pb[nt][1]);
+                }
+              }
+            }
+          }
+        }
+      }
+    }
+    // ---- the end of the unit or of the run -----------------------------------------------------
+    const bool unit_ends = at.j + 1 == at.nt;
+    if (unit_ends || i + 1 == n) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], d);
+      if constexpr (KIND == SPEAR_KV_INT4) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[a][nt][e] = fmaf(-kInt4Offset, psum[nt][e & 1], acc[a][nt][e]);
+      }
+      const bool whole = unit_ends && from == 0;
+      if (!unit_ends) {
+        // every copy is in and read: the ring is this piece's place
+        cp_wait(0);
+        __syncwarp();
+      }
+      float* dst = unit_ends ? first_piece : last_piece;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = nt * 8 + 2 * cl + e;
+          if (h < gn) {
+            if (whole) {
+              const float inv = 1.f / l[nt][e];
+              __nv_bfloat16* o = p.out + at.b * p.ld_out + (long long)(h0 + h) * DIM;
+#pragma unroll
+              for (int a = 0; a < MT; a += 4) {
+                const int d = (a / (L::VL / 2)) * 8 * L::VL + rho * L::VL + 2 * (a % (L::VL / 2));
+                uint4 w;
+                w.x = pack_bf16x2(acc[a][nt][e] * inv, acc[a][nt][e + 2] * inv);
+                w.y = pack_bf16x2(acc[a + 1][nt][e] * inv, acc[a + 1][nt][e + 2] * inv);
+                w.z = pack_bf16x2(acc[a + 2][nt][e] * inv, acc[a + 2][nt][e + 2] * inv);
+                w.w = pack_bf16x2(acc[a + 3][nt][e] * inv, acc[a + 3][nt][e + 2] * inv);
+                *reinterpret_cast<uint4*>(o + d) = w;
+              }
+              if (p.lse && rho == 0)
+                p.lse[(long long)at.b * p.heads + h0 + h] = (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
+            } else {
+#pragma unroll
+              for (int a = 0; a < MT; ++a) {
+                const int d = (a / (L::VL / 2)) * 8 * L::VL + rho * L::VL + 2 * (a % (L::VL / 2));
+                *reinterpret_cast<float2*>(dst + h * DIM + d) = make_float2(acc[a][nt][e], acc[a][nt][e + 2]);
+              }
+              if (rho == 0) {
+                dst[gn * DIM + h] = m[nt][e];
+                dst[gn * DIM + gn + h] = l[nt][e];
+              }
+            }
+          }
+        }
+      if (!whole && lane == 0)
+        pieces[2 * warp + (unit_ends ? 0 : 1)] = {t0 + i - at.j, at.nt, at.b * units + at.u, from, at.j + 1};
+    }
+    advance<TILE>(p, units, at);
   }
+  cp_wait(0);
+  __syncthreads();
+
+  // ---- join the pieces of each unit ---------------------------------------------------------------
+  auto piece_at = [&](int i) -> float* {
+    uint8_t* r = smem + (size_t)(i >> 1) * (ring_bytes + p.piece * 4);
+    return reinterpret_cast<float*>(i & 1 ? r : r + ring_bytes);
+  };
+  // value of element (h, d) over pieces at(0..count), with the common maximum and sum
+  auto finish = [&](const Piece& pc, int count, auto global, auto at_piece, float* part) {
+    // pieces of other CTAs are read past this SM's L1
+    auto get = [](const float* f) {
+      if constexpr (decltype(global)::value) return __ldcg(f);
+      else return *f;
+    };
+    auto get4 = [](const float* f) {
+      if constexpr (decltype(global)::value) return __ldcg(reinterpret_cast<const float4*>(f));
+      else return *reinterpret_cast<const float4*>(f);
+    };
+    const int u = pc.unit % units, b = pc.unit / units;
+    const int head = u / p.blocks, blk = u - head * p.blocks;
+    const int h0 = head * p.group + blk * 8 * NT, gn = min(8 * NT, p.group - blk * 8 * NT);
+    for (int i = tid; i < gn * (DIM / 4); i += W * 32) {
+      const int h = i / (DIM / 4), d = (i % (DIM / 4)) * 4;
+      float mx = -INFINITY, sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < count; ++k) mx = fmaxf(mx, get(at_piece(k) + gn * DIM + h));
+#pragma unroll 4
+      for (int k = 0; k < count; ++k) {
+        const float* f = at_piece(k);
+        const float w = exp2_(get(f + gn * DIM + h) - mx);
+        const float4 v = get4(f + h * DIM + d);
+        sum = fmaf(w, get(f + gn * DIM + gn + h), sum);
+        o.x = fmaf(w, v.x, o.x);
+        o.y = fmaf(w, v.y, o.y);
+        o.z = fmaf(w, v.z, o.z);
+        o.w = fmaf(w, v.w, o.w);
+      }
+      if (part) {
+        __stcg(reinterpret_cast<float4*>(part + h * DIM + d), o);
+        if (d == 0) {
+          __stcg(part + gn * DIM + h, mx);
+          __stcg(part + gn * DIM + gn + h, sum);
+        }
+      } else {
+        const float inv = 1.f / sum;
+        *reinterpret_cast<uint2*>(p.out + b * p.ld_out + (long long)(h0 + h) * DIM + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (p.lse && d == 0) p.lse[(long long)b * p.heads + h0 + h] = (mx + log2f(sum)) * 0.6931471805599453f;
+      }
+    }
+  };
+  if (tid == 0) {
+    int k = 0;
+    for (int i = 0; i < 2 * W; ++i)
+      if (pieces[i].unit >= 0) order[k++] = i;
+    for (; k < 2 * W; ++k) order[k] = -1;
+    joins[0] = joins[1] = 0;
+  }
+  __syncthreads();
+  Piece open[2];
+  open[0].unit = open[1].unit = -1;
+  for (int k = 0; k < 2 * W && order[k] >= 0;) {
+    const Piece pc = pieces[order[k]];
+    int e = k + 1;
+    while (e < 2 * W && order[e] >= 0 && pieces[order[e]].unit == pc.unit) ++e;
+    const bool starts = pc.from == 0, ends = pieces[order[e - 1]].to == pc.nt;
+    const int side = starts ? 1 : 0;  // its place among the CTA's parts, if it is open
+    float* part = starts && ends ? nullptr : p.parts + ((size_t)blockIdx.x * 2 + side) * p.piece;
+    finish(pc, e - k, std::false_type{}, [&](int i) { return piece_at(order[k + i]); }, part);
+    if (part) open[side] = pc;
+    k = e;
+  }
+  if (open[0].unit < 0 && open[1].unit < 0) return;
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    for (int side = 0; side < 2; ++side)
+      if (open[side].unit >= 0) {
+        const int c0 = split.owner(open[side].start) / W, c1 = split.owner(open[side].start + open[side].nt - 1) / W;
+        joins[side] = atomicAdd(p.tickets + c0, 1) == c1 - c0;
+        if (joins[side]) p.tickets[c0] = 0;
+      }
+    __threadfence();
+  }
+  __syncthreads();
+  for (int side = 0; side < 2; ++side)
+    if (joins[side]) {
+      const int c0 = split.owner(open[side].start) / W, c1 = split.owner(open[side].start + open[side].nt - 1) / W;
+      finish(open[side], c1 - c0 + 1, std::true_type{},
+             [&](int i) { return p.parts + ((size_t)(c0 + i) * 2 + (i == 0)) * p.piece; }, nullptr);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr int attn_warps(int kind, int dim) { return kind == SPEAR_KV_BF16 && dim == 256 ? 4 : 8; }
+constexpr int attn_per_sm(int kind, int dim, int nt) { return kind != SPEAR_KV_BF16 && dim < 256 && nt == 1 ? 2 : 1; }
+
+struct AttnPlan {
+  int nt, blocks, piece;
+  int ctas;  // at most
+};
+
+static AttnPlan plan_attn(const KvView& c, int n_q_heads) {
+  AttnPlan a;
+  const int group = n_q_heads / c.heads;
+  a.nt = group > 8 && c.dim < 256 ? 2 : 1;
+  a.blocks = (group + 8 * a.nt - 1) / (8 * a.nt);
+  const int in_unit = group < 8 * a.nt ? group : 8 * a.nt;
+  a.piece = (in_unit * (c.dim + 2) + 3) / 4 * 4;
+  a.ctas = device_sm_count() * attn_per_sm(c.kind, c.dim, a.nt);
+  return a;
+}
+
+static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+static size_t attn_ws_bytes(const AttnPlan& a) {
+  return kWsHeaderBytes + up256(a.ctas * sizeof(int)) + up256((size_t)a.ctas * 2 * a.piece * sizeof(float));
+}
+
+template <int KIND, int DIM, int NT>
+static cudaError_t launch_attn(AttnArgs& a, const AttnPlan& pl, cudaStream_t st) {
+  using L = Lay<KIND, DIM>;
+  constexpr int W = attn_warps(KIND, DIM), PER_SM = attn_per_sm(KIND, DIM, NT);
+  // 227 KB per SM less 1 KB that each CTA takes besides, and 2 KB for the kernel's static arrays
+  constexpr size_t kRoom = PER_SM == 2 ? 227 * 512 - 1024 - 2048 : 227 * 1024 - 2048;
+  a.stages = (int)((kRoom / W - (size_t)a.piece * 4) / L::STAGE);
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  // at least two stages, whose place a piece takes over at the end
+  if (a.stages < 2 || (size_t)a.stages * L::STAGE < (size_t)a.piece * 4) return cudaErrorInvalidConfiguration;
+  size_t smem = (size_t)W * (a.stages * L::STAGE + (size_t)a.piece * 4);
+  const size_t line = sizeof(long long) * (a.n_seqs + 1);
+  if (smem < line) smem = line;
+  auto* k = attn_kernel<KIND, DIM, NT, W, PER_SM>;
+  static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  // no more CTAs than the longest possible line gives work to
+  const long long tiles = (long long)a.c.heads * a.blocks * a.n_seqs * ((a.max_len + L::TILE - 1) / L::TILE);
+  const long long need = (tiles + (long long)kMinTiles * W - 1) / ((long long)kMinTiles * W);
+  const int grid = (int)(need < pl.ctas ? need : pl.ctas);
+  k<<<grid, W * 32, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace spear
@@ -113,7 +778,7 @@ using namespace spear;
 extern "C" size_t spear_attn_workspace_bytes(const spear_kv_cache* cache, int n_q_heads) {
   KvView c;
   if (check_kv_cache(cache, &c) != SPEAR_OK || n_q_heads < 1 || n_q_heads > 1024 || n_q_heads % c.heads) return 0;
-  return kWsHeaderBytes;
+  return attn_ws_bytes(plan_attn(c, n_q_heads));
 }
 
 extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q, long long ld_q, int n_seqs,
@@ -135,8 +800,8 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   if (q == out) return set_error(SPEAR_ERR_INVALID_ARG, "q and out are the same buffer");
   if (max_pages < 1 || ld_table < max_pages)
     return set_error(SPEAR_ERR_INVALID_ARG, "max_pages=%d ld_table=%d: 1 <= max_pages <= ld_table", max_pages, ld_table);
-  if ((long long)max_pages * a.c.page_size > 0x7fffffffLL)
-    return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "max_pages=%d: a sequence holds less than 2^31 tokens", max_pages);
+  if ((long long)max_pages * a.c.page_size > 0x7fff0000LL)
+    return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "max_pages=%d: a sequence holds less than 2^31 - 2^16 tokens", max_pages);
   const long long row = (long long)n_q_heads * a.c.dim;
   if (ld_q < row || ld_out < row || ld_q % 8 || ld_out % 8)
     return set_error(SPEAR_ERR_INVALID_ARG, "ld_q=%lld ld_out=%lld: multiples of 8 of at least %lld", ld_q, ld_out, row);
@@ -145,7 +810,8 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   for (const void* p : {(const void*)page_table, (const void*)seq_lens, (const void*)lse})
     if (reinterpret_cast<uintptr_t>(p) & 3u)
       return set_error(SPEAR_ERR_ALIGNMENT, "page_table, seq_lens and lse must be 4-byte aligned");
-  const size_t need = spear_attn_workspace_bytes(cache, n_q_heads);
+  const AttnPlan pl = plan_attn(a.c, n_q_heads);
+  const size_t need = attn_ws_bytes(pl);
   if (ws_bytes < need) return set_error(SPEAR_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
@@ -155,16 +821,25 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   a.ld_q = ld_q;
   a.ld_out = ld_out;
   a.ld_table = ld_table;
-  a.max_pages = max_pages;
+  a.max_len = max_pages * a.c.page_size;
   a.n_seqs = n_seqs;
   a.heads = n_q_heads;
   a.group = n_q_heads / a.c.heads;
-  a.scale = scale;
-  a.hdr = static_cast<WsHeader*>(ws);
+  a.blocks = pl.blocks;
+  a.piece = pl.piece;
+  a.scale = scale * 1.4426950408889634f;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.hdr = reinterpret_cast<WsHeader*>(w);
+  a.tickets = reinterpret_cast<int*>(w + kWsHeaderBytes);
+  a.parts = reinterpret_cast<float*>(w + kWsHeaderBytes + up256(pl.ctas * sizeof(int)));
+  cudaError_t e = cudaErrorInvalidValue;
   for_kind_dim(a.c.kind, a.c.dim, [&](auto kc, auto dc) {
-    attn_kernel<kc.value, dc.value>
-        <<<dim3(n_q_heads, n_seqs), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    if constexpr (dc.value < 256)
+      if (pl.nt == 2) {
+        e = launch_attn<kc.value, dc.value, 2>(a, pl, static_cast<cudaStream_t>(stream));
+        return;
+      }
+    e = launch_attn<kc.value, dc.value, 1>(a, pl, static_cast<cudaStream_t>(stream));
   });
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SPEAR_OK : set_cuda_error("attention launch", e);
 }
