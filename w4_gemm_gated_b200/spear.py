@@ -364,13 +364,14 @@ class KVCache:
 
     def __post_init__(self):
         quant = self.kind != KV_BF16
-        self.device = self.k.device
+        self.device, self.index = self.k.device, self.k.get_device()
         self.struct = KVCacheStruct(
             self.kind, self.n_pages, self.page_size, self.n_heads, self.head_dim, self.k.data_ptr(), self.v.data_ptr(),
             self.k_scales.data_ptr() if quant else None, self.v_scales.data_ptr() if quant else None,
             self.k.stride(0) * self.k.element_size() if self.n_pages > 1 else 0,
             self.k_scales.stride(0) if quant and self.n_pages > 1 else 0)
-        self._ref = ctypes.byref(self.struct)
+        self.ref = ctypes.byref(self.struct)
+        self.tensors = tuple(t for t in (self.k, self.v, self.k_scales, self.v_scales) if t is not None)
 
 
 def _dense_pages(t: torch.Tensor) -> bool:
@@ -431,43 +432,65 @@ def make_kv_cache(kind: int, n_pages: int, page_size: int, n_heads: int, head_di
     return kv_cache_from_parts(k, v, ks, vs)
 
 
-def _call(device: torch.device, stream, tensors, fn) -> None:
-    """fn(raw stream) on `device`, whichever device is current: on its current
-    stream, or on `stream`, whose use of the tensors the allocator is told."""
-    if stream is not None:
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device index; torch.cuda.current_stream() costs 3 us
+
+
+def _launch(index: int, stream, tensors, fn, *args) -> None:
+    """fn(*args, stream) on device `index`, whichever is current: on its current
+    stream, or on `stream`, whose use of the tensors the allocator is told.
+    These calls are short: the path with neither is kept straight."""
+    if stream is None:
+        if index == torch.cuda.current_device():
+            rc = fn(*args, _raw_stream(index))
+        else:
+            with torch.cuda.device(index):
+                rc = fn(*args, _raw_stream(index))
+    else:
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-    if device.index == torch.cuda.current_device():
-        _check(fn(stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream))
-        return
-    with torch.cuda.device(device):
-        _check(fn(stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream))
+        with torch.cuda.device(index):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != OK:
+        _check(rc)
 
 
-def _on(device: torch.device, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors must live on one CUDA device: got {t.device} beside {device}")
+def _new(like: torch.Tensor, stream, shape=None) -> torch.Tensor:
+    """A dense bf16 output on like's device, of its shape or `shape`, allocated on the stream that writes it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _new(like, None, shape)
+    if shape is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
 
 
-def _rows(t: torch.Tensor, n_heads: int, head_dim: int, what: str) -> int:
-    """Elements between the rows of n_heads x head_dim bf16 values of t (2-D or 3-D)."""
-    if t.dtype != torch.bfloat16:
+def _rows(t: torch.Tensor, index: int, n: int, n_heads: int, head_dim: int, what: str) -> int:
+    """Elements between the rows of t: n rows of n_heads x head_dim bf16 values (2-D or 3-D)."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{what} must be bf16")
-    row = n_heads * head_dim
-    if t.dim() == 3:
-        ok = t.shape[1:] == (n_heads, head_dim) and t.stride(2) == 1 and (n_heads == 1 or t.stride(1) == head_dim)
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape == (n, n_heads, head_dim) and strides[2] == 1 and (strides[1] == head_dim or n_heads == 1)
     else:
-        ok = t.dim() == 2 and t.shape[1] == row and t.stride(1) == 1
+        ok = shape == (n, n_heads * head_dim) and strides[1] == 1
     if not ok:
-        raise ValueError(f"{what} must have rows of {n_heads} x {head_dim} consecutive values")
-    return t.stride(0) if t.shape[0] > 1 else row
+        raise ValueError(f"{what} must be {n} rows of {n_heads} x {head_dim} consecutive values")
+    if t.get_device() != index:
+        raise ValueError(f"{what} must live on the cache's device")
+    return strides[0] if n > 1 else n_heads * head_dim
 
 
-def _i32(t: torch.Tensor, n: int, what: str) -> None:
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be {n} contiguous int32 values")
+def _i32(t: torch.Tensor, index: int, n: int, what: str) -> int:
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{what} must be {n} contiguous int32 values on the cache's device")
+    return t.data_ptr()
+
+
+def _ws(t: torch.Tensor, index: int) -> tuple[int, int]:
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous, on the cache's device")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, ws: torch.Tensor,
@@ -475,46 +498,36 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     """Write n new tokens' keys and values (n x n_heads x head_dim or n x (n_heads
     * head_dim) bf16; rows may be ranges of wider rows) at their slots (int32,
     page * page_size + offset; negative: skipped; no slot twice)."""
-    n = k.shape[0]
-    ld_k, ld_v = (_rows(t, cache.n_heads, cache.head_dim, w) for t, w in ((k, "k"), (v, "v")))
-    if v.shape[0] != n:
-        raise ValueError("k and v must have one row per slot")
-    _i32(slots, n, "slots")
-    _on(cache.device, k, v, slots, ws)
-    kp, vp, sp, wp, wn = k.data_ptr(), v.data_ptr(), slots.data_ptr(), _ptr(ws), ws.numel() * ws.element_size()
-    _call(cache.device, stream, (k, v, slots, ws, cache.k, cache.v, cache.k_scales, cache.v_scales),
-          lambda st: F["spear_kv_write"](cache._ref, kp, ld_k, vp, ld_v, sp, n, wp, wn, st))
+    n, di, G, D = k.shape[0], cache.index, cache.n_heads, cache.head_dim
+    ld_k, ld_v = _rows(k, di, n, G, D, "k"), _rows(v, di, n, G, D, "v")
+    sp = _i32(slots, di, n, "slots")
+    wp, wn = _ws(ws, di)
+    _launch(di, stream, (k, v, slots, ws, *cache.tensors), _kv_write, cache.ref, k.data_ptr(), ld_k, v.data_ptr(),
+            ld_v, sp, n, wp, wn)
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, ws: torch.Tensor, k_out: torch.Tensor | None = None,
             v_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The keys and values at n slots, n x n_heads x head_dim bf16 (a negative slot reads as zeros)."""
-    n = slots.shape[0]
-    _i32(slots, n, "slots")
-    shape = (n, cache.n_heads, cache.head_dim)
-    k_out, v_out = _outputs(cache.device, stream, shape, k_out, v_out)
-    for t in (k_out, v_out):
-        if t.dtype != torch.bfloat16 or t.numel() != n * cache.n_heads * cache.head_dim:
-            raise ValueError(f"k_out and v_out must be bf16 of shape {shape}")
-    _on(cache.device, slots, ws, k_out, v_out)
-    kp, vp, sp, wp, wn = _ptr(k_out), _ptr(v_out), slots.data_ptr(), _ptr(ws), ws.numel() * ws.element_size()
-    _call(cache.device, stream, (slots, ws, k_out, v_out, cache.k, cache.v, cache.k_scales, cache.v_scales),
-          lambda st: F["spear_kv_read"](cache._ref, sp, n, kp, vp, wp, wn, st))
+    n, di, G, D = slots.shape[0], cache.index, cache.n_heads, cache.head_dim
+    sp = _i32(slots, di, n, "slots")
+    wp, wn = _ws(ws, di)
+    if k_out is None:
+        k_out = _new(slots, stream, (n, G, D))
+    elif k_out.dtype is not torch.bfloat16 or _rows(k_out, di, n, G, D, "k_out") != G * D:
+        raise ValueError("k_out must be contiguous bf16")
+    if v_out is None:
+        v_out = _new(slots, stream, (n, G, D))
+    elif v_out.dtype is not torch.bfloat16 or _rows(v_out, di, n, G, D, "v_out") != G * D:
+        raise ValueError("v_out must be contiguous bf16")
+    _launch(di, stream, (slots, ws, k_out, v_out, *cache.tensors), _kv_read, cache.ref, sp, n, k_out.data_ptr(),
+            v_out.data_ptr(), wp, wn)
     return k_out, v_out
 
 
-def _outputs(device, stream, shape, *given):
-    """The given bf16 outputs, with the missing ones allocated on the stream that writes them."""
-    if all(t is not None for t in given):
-        return given
-    if stream is None:
-        return tuple(torch.empty(shape, dtype=torch.bfloat16, device=device) if t is None else t for t in given)
-    with torch.cuda.stream(stream):
-        return _outputs(device, None, shape, *given)
-
-
 def attn_workspace_bytes(cache: KVCache, n_q_heads: int) -> int:
-    n = F["spear_attn_workspace_bytes"](cache._ref, n_q_heads)
+    with torch.cuda.device(cache.index):
+        n = F["spear_attn_workspace_bytes"](cache.ref, n_q_heads)
     if n == 0:
         raise SpearError(ERR_UNSUPPORTED_SHAPE, f"n_q_heads={n_q_heads} over a cache of {cache.n_heads} heads")
     return n
@@ -524,7 +537,7 @@ def make_attn_workspace(cache: KVCache, n_q_heads: int, stream=None) -> torch.Te
     """A workspace for attn_decode (any batch), kv_write and kv_read on this cache or others of its shape."""
     n = attn_workspace_bytes(cache, n_q_heads)
     ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
-    _call(cache.device, stream, (ws,), lambda st: F["spear_workspace_init"](ws.data_ptr(), n, st))
+    _launch(cache.index, stream, (ws,), F["spear_workspace_init"], ws.data_ptr(), n)
     return ws
 
 
@@ -536,30 +549,39 @@ def attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_l
     rows may be ranges of wider rows; page_table: n_seqs x max_pages int32;
     seq_lens: int32; scale: 1 / sqrt(head_dim) if None; lse: optional fp32
     n_seqs x n_q_heads, written.  Returns out, of q's shape."""
-    n = q.shape[0]
-    D = cache.head_dim
-    H = q.shape[1] if q.dim() == 3 else q.shape[1] // D
-    ld_q = _rows(q, H, D, "q")
+    shape, di, D = q.shape, cache.index, cache.head_dim
+    n = shape[0]
+    H = shape[1] if len(shape) == 3 else shape[1] // D
+    ld_q = _rows(q, di, n, H, D, "q")
     if out is None:
-        out, = _outputs(cache.device, stream, q.shape, None)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    ld_out = _rows(out, H, D, "out")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n \
-            or page_table.stride(1) != 1 and page_table.shape[1] > 1:
-        raise ValueError("page_table must be n_seqs x max_pages int32 with consecutive rows")
-    _i32(seq_lens, n, "seq_lens")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, H) or not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous fp32, n_seqs x n_q_heads")
-    _on(cache.device, q, out, page_table, seq_lens, lse, ws)
-    pages = page_table.shape[1]
-    ld_table = page_table.stride(0) if n > 1 else pages
-    args = (q.data_ptr(), ld_q, n, H, page_table.data_ptr(), pages, ld_table, seq_lens.data_ptr(),
-            D ** -0.5 if scale is None else scale, out.data_ptr(), ld_out,
-            None if lse is None else lse.data_ptr(), _ptr(ws), ws.numel() * ws.element_size())
-    _call(cache.device, stream, (q, out, page_table, seq_lens, lse, ws, cache.k, cache.v, cache.k_scales,
-                                 cache.v_scales), lambda st: F["spear_attn_decode"](cache._ref, *args, st))
+        out, ld_out = _new(q, stream), H * D
+    else:
+        if out.shape != shape:
+            raise ValueError("out must have q's shape")
+        ld_out = _rows(out, di, n, H, D, "out")
+    t_shape, t_strides = page_table.shape, page_table.stride()
+    if page_table.dtype is not torch.int32 or len(t_shape) != 2 or t_shape[0] != n \
+            or t_strides[1] != 1 and t_shape[1] > 1 or page_table.get_device() != di:
+        raise ValueError("page_table must be n_seqs x max_pages int32 with consecutive rows, on the cache's device")
+    pages = t_shape[1]
+    lp = _i32(seq_lens, di, n, "seq_lens")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, H) or not lse.is_contiguous()
+                            or lse.get_device() != di):
+        raise ValueError("lse must be contiguous fp32, n_seqs x n_q_heads, on the cache's device")
+    wp, wn = _ws(ws, di)
+    _launch(di, stream, (q, out, page_table, seq_lens, lse, ws, *cache.tensors), _attn_decode, cache.ref, q.data_ptr(),
+            ld_q, n, H, page_table.data_ptr(), pages, t_strides[0] if n > 1 else pages, lp,
+            D ** -0.5 if scale is None else scale, out.data_ptr(), ld_out, None if lse is None else lse.data_ptr(),
+            wp, wn)
     return out
+
+
+def _norm_ptr(t: torch.Tensor | None, shape, index: int, what: str) -> int | None:
+    if t is None:
+        return None
+    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{what} must be contiguous bf16 of shape {tuple(shape)}, on x's CUDA device")
+    return t.data_ptr()
 
 
 def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, pre_weight: torch.Tensor | None = None,
@@ -571,34 +593,44 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, pre_weight: to
     x_out = residual_scale x + block_scale gate norm(y; post_weight),
     h = norm(x_out; pre_weight); with no post_weight y is taken as it is, with
     no y h = norm(x).  x, y: M x K bf16; weights K; gate K, 1 x K or M x K bf16 (rows
-    may lie apart).  Returns (x_out, h), (x, h) without y; x_out=x updates x in place."""
-    if x.dim() != 2:
-        raise ValueError("x must be M x K")
-    M, K = x.shape
-    for t, what, shape in ((x, "x", (M, K)), (y, "y", (M, K)), (x_out, "x_out", (M, K)), (h, "h", (M, K)),
-                           (pre_weight, "pre_weight", (K,)), (post_weight, "post_weight", (K,))):
-        if t is not None and (t.dtype != torch.bfloat16 or t.shape != shape):
-            raise ValueError(f"{what} must be bf16 of shape {shape}")
-    gate_ld = 0
+    may lie apart).  Returns (x_out, h), (x, h) without y; x_out=x updates x in
+    place; norm=False leaves the norm out (after the last block) and returns (x_out, None)."""
+    shape, di = x.shape, x.get_device()
+    if len(shape) != 2 or di < 0:
+        raise ValueError("x must be M x K on a CUDA device")
+    M, K = shape
+    xp, yp = _norm_ptr(x, shape, di, "x"), _norm_ptr(y, shape, di, "y")
+    post, pre = _norm_ptr(post_weight, (K,), di, "post_weight"), _norm_ptr(pre_weight, (K,), di, "pre_weight")
+    gp, gate_ld = None, 0
     if gate is not None:
-        rows = gate.view(1, K) if gate.dim() == 1 and gate.shape[0] == K else gate
-        if rows.dtype != torch.bfloat16 or rows.dim() != 2 or rows.shape[1] != K or rows.shape[0] not in (1, M) \
-                or rows.stride(1) != 1 and K > 1:
-            raise ValueError("gate must be bf16, K, 1 x K or M x K, with consecutive rows")
-        gate_ld = rows.stride(0) if rows.shape[0] > 1 else 0
-    if y is not None:
-        if x_out is None:
-            x_out, = _outputs(x.device, stream, (M, K), None)
+        g_shape, g_strides = gate.shape, gate.stride()
+        if gate.dtype is not torch.bfloat16 or g_shape not in ((K,), (1, K), (M, K)) or g_strides[-1] != 1 \
+                or gate.get_device() != di:
+            raise ValueError("gate must be bf16, K, 1 x K or M x K, with consecutive rows, on x's device")
+        gp = gate.data_ptr()
+        if len(g_shape) == 2 and g_shape[0] > 1:
+            gate_ld = g_strides[0]
+    if x_out is not None:
+        op = _norm_ptr(x_out, shape, di, "x_out")
+    elif y is not None:
+        x_out = _new(x, stream)
+        op = x_out.data_ptr()
+    else:
+        op = None
     if not norm:
-        h = None
-    elif h is None:
-        h, = _outputs(x.device, stream, (M, K), None)
-    _on(x.device, y, pre_weight, post_weight, gate, x_out, h)
-    args = (_ptr(x), _ptr(y), M, K, _ptr(post_weight), None if gate is None else gate.data_ptr(), gate_ld,
-            residual_scale, block_scale, _ptr(pre_weight), eps, _ptr(x_out), _ptr(h))
-    _call(x.device, stream, (x, y, pre_weight, post_weight, gate, x_out, h),
-          lambda st: F["spear_block_norm"](*args, st))
+        h = hp = None
+    elif h is not None:
+        hp = _norm_ptr(h, shape, di, "h")
+    else:
+        h = _new(x, stream)
+        hp = h.data_ptr()
+    _launch(di, stream, (x, y, pre_weight, post_weight, gate, x_out, h), _block_norm, xp, yp, M, K, post, gp, gate_ld,
+            residual_scale, block_scale, pre, eps, op, hp)
     return (x if y is None else x_out), h
+
+
+_kv_write, _kv_read = F["spear_kv_write"], F["spear_kv_read"]
+_attn_decode, _block_norm = F["spear_attn_decode"], F["spear_block_norm"]
 
 
 def test_inject_timeout(kernel: int, wait_cycles: int = 0) -> None:
