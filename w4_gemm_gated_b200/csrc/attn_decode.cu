@@ -7,10 +7,11 @@
 //
 // Work.  A unit is one (sequence, kv head) with up to 8 NT query heads; its
 // tokens are cut into tiles of TILE.  All units' tiles in order form one line,
-// which is cut into equal runs, one per warp, by the lengths alone (every CTA
-// sums them up): ragged batches load the machine evenly, a long sequence is
-// spread over many warps, and a warp takes many short ones without meeting
-// anybody.  A warp streams its run through its own ring of shared-memory
+// which is cut into equal runs, one per CTA and in it one per warp, by the
+// lengths alone (every CTA sums them up): ragged batches load the machine
+// evenly, a long sequence is spread over many warps, and a warp takes many
+// short ones without meeting anybody.  Where every unit is short the CTAs'
+// borders move to units' borders (see Cut).  A warp streams its run through its own ring of shared-memory
 // stages (16-byte asynchronous copies, rows past a sequence's end filled with
 // zeros), so that copies cross the units' borders and never wait for another
 // warp.
@@ -55,7 +56,8 @@ struct AttnArgs {
   float* parts;  // two pieces per CTA
 };
 
-constexpr int kMinTiles = 2;  // tiles a warp should have before more warps take part
+constexpr int kMinTiles = 2;  // tiles a warp should have before more CTAs take part
+constexpr int kShort = 4;     // tiles per warp up to which a unit stays in one CTA
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -172,13 +174,24 @@ struct Piece {
   int from, to;     // tiles [from, to)
 };
 
-struct Split {
-  long long q;  // tiles per worker, the first `more` of them one more
-  int more;
+// a / b for a >= 0, b > 0 (the 64-bit division takes several times as long)
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return (unsigned long long)a >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
+// `total` tiles cut into `parts` runs of q or q + 1.
+struct Cut {
+  long long q;
+  int more;  // the first `more` runs are one longer
+  __device__ __forceinline__ Cut(long long total, int parts) {
+    q = quotient(total, parts);
+    more = (int)(total - q * parts);
+  }
   __device__ __forceinline__ long long begin(int w) const { return q * w + min(w, more); }
-  __device__ __forceinline__ int owner(long long t) const {
+  __device__ __forceinline__ int owner(long long t) const {  // q > 0
     const long long border = (q + 1) * more;
-    return t < border ? (int)(t / (q + 1)) : more + (int)((t - border) / q);
+    // q + 1 fits an int wherever a run does
+    return (int)(t < border ? quotient(t, (int)q + 1) : more + quotient(t - border, (int)q));
   }
 };
 
@@ -187,25 +200,27 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   using L = Lay<KIND, DIM>;
   constexpr int TILE = L::TILE, TS = L::TS, RB = L::RB, MT = DIM / 16;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long scan_warp[W], line;
+  __shared__ long long scan_sum[W];
+  __shared__ int scan_max[W];
   __shared__ Piece pieces[2 * W];  // a warp's first (unit begun before it), its last
-  __shared__ int order[2 * W];
   __shared__ int joins[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rho = lane >> 2, cl = lane & 3;
   const int units = p.c.heads * p.blocks;
 
   // ---- the line: tiles before each sequence --------------------------------------
   long long* before = reinterpret_cast<long long*>(smem);  // n_seqs + 1 of them, in the rings' place
-  const int per = (p.n_seqs + W * 32 - 1) / (W * 32);
+  int longest = 0;                                         // tiles of the longest unit
   {
-    long long sum = 0;
+    const int per = (p.n_seqs + W * 32 - 1) / (W * 32);
     const int b0 = tid * per, b1 = min(b0 + per, p.n_seqs);
+    long long sum = 0;
     for (int b = b0; b < b1; ++b) {
-      if (blockIdx.x == 0) {
-        const int n = __ldg(p.lens + b);
-        if (n < 0 || n > p.max_len) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
-      }
-      sum += (clamp_len(p, b) + TILE - 1) / TILE;
+      const int n = __ldg(p.lens + b);
+      if (blockIdx.x == 0 && (n < 0 || n > p.max_len)) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
+      const int nt = (min(max(n, 0), p.max_len) + TILE - 1) / TILE;
+      before[b] = nt;
+      sum += nt;
+      longest = max(longest, nt);
     }
     long long inc = sum;
 #pragma unroll
@@ -213,18 +228,27 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
       if (lane >= d) inc += o;
     }
-    if (lane == 31) scan_warp[warp] = inc;
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    if (lane == 31) scan_sum[warp] = inc, scan_max[warp] = longest;
+    if (lane < 2) pieces[2 * warp + lane].unit = -1;
+    if (tid < 2) joins[tid] = 0;
     __syncthreads();
-    long long off = inc - sum;
-    for (int w = 0; w < warp; ++w) off += scan_warp[w];
-    for (int b = b0; b < b1; ++b) {
-      before[b] = off;
-      off += (clamp_len(p, b) + TILE - 1) / TILE;
+    long long off = inc - sum, all = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) off += scan_sum[w];
+      all += scan_sum[w];
+      longest = max(longest, scan_max[w]);
     }
-    if (tid == W * 32 - 1) before[p.n_seqs] = line = off;
+    for (int b = b0; b < b1; ++b) {
+      const long long nt = before[b];
+      before[b] = off;
+      off += nt;
+    }
+    if (tid == 0) before[p.n_seqs] = all;
     __syncthreads();
   }
-  const long long total = line * units;
+  const long long total = before[p.n_seqs] * units;
   // sequences without tokens
   for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x)
     if (before[b] == before[b + 1]) {
@@ -233,32 +257,48 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       if (p.lse)
         for (int h = tid; h < p.heads; h += W * 32) p.lse[(long long)b * p.heads + h] = -INFINITY;
     }
-  // ---- this warp's run -------------------------------------------------------------
-  const int workers = (int)min((long long)gridDim.x * W, (total + kMinTiles - 1) / kMinTiles);
-  if ((int)blockIdx.x * W >= workers) return;  // nothing for the whole CTA
-  Split split;
-  split.q = total / workers;
-  split.more = (int)(total - split.q * workers);
-  const int worker = blockIdx.x * W + warp;
-  const long long t0 = worker < workers ? split.begin(worker) : 0;
-  const int n = worker < workers ? (int)(split.begin(worker + 1) - t0) : 0;
-  Place in = {};  // next tile to copy
-  if (n > 0) {
-    int lo = 0, hi = p.n_seqs;  // before[lo] * units <= t0 < before[hi] * units
+  // ---- this CTA's and this warp's run -----------------------------------------------
+  // Where no unit is longer than kShort tiles per warp of a CTA, CTAs take whole
+  // units: the borders of even runs move on to the next unit's start.  A CTA
+  // may then have up to kShort tiles per warp more than its share, which
+  // costs no more than joining a unit across CTAs does, and saves that join.
+  const bool aligned = longest <= kShort * W;
+  const int ctas = (int)(aligned ? min((long long)gridDim.x, min(total, (long long)p.n_seqs * units))
+                                 : min((long long)gridDim.x, quotient(total + kMinTiles * W - 1, kMinTiles * W)));
+  if ((int)blockIdx.x >= ctas) return;  // nothing for this CTA
+  auto place = [&](long long t) {       // of tile t < total
+    Place c;
+    int lo = 0, hi = p.n_seqs;  // before[lo] * units <= t < before[hi] * units
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (before[mid] * units <= t0) lo = mid;
+      if (before[mid] * units <= t) lo = mid;
       else hi = mid;
     }
-    in.b = lo;
-    in.len = clamp_len(p, lo);
-    in.nt = (in.len + TILE - 1) / TILE;
-    const long long r = t0 - before[lo] * units;
-    in.u = (int)(r / in.nt);
-    in.j = (int)(r - (long long)in.u * in.nt);
+    c.b = lo;
+    c.len = clamp_len(p, lo);
+    c.nt = (int)(before[lo + 1] - before[lo]);
+    const long long r = t - before[lo] * units;
+    c.u = (int)quotient(r, c.nt);
+    c.j = (int)(r - (long long)c.u * c.nt);
+    return c;
+  };
+  const Cut cut(total, ctas);
+  long long c_begin = cut.begin(blockIdx.x), c_end = cut.begin(blockIdx.x + 1);
+  if (aligned) {
+    auto up = [&](long long t) {  // the next unit's start from t on
+      if (t >= total) return total;
+      const Place c = place(t);
+      return c.j ? t + c.nt - c.j : t;
+    };
+    c_begin = up(c_begin);
+    c_end = up(c_end);
   }
+  const Cut mine(c_end - c_begin, W);
+  const long long t0 = c_begin + mine.begin(warp);
+  const int n = (int)(mine.begin(warp + 1) - mine.begin(warp));
+  Place in = {};  // next tile to copy
+  if (n > 0) in = place(t0);
   Place at = in;  // tile to work on
-  if (lane == 0) pieces[2 * warp].unit = pieces[2 * warp + 1].unit = -1;
   __syncthreads();  // the rings take over `before`'s place
 
   const int ring_bytes = p.stages * L::STAGE;
@@ -267,14 +307,16 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   float* last_piece = reinterpret_cast<float*>(ring);  // once the run is through
   const uint32_t ring_a = smem_u32(ring);
 
-  int page[TS];  // pages of the next tile to copy
-  auto load_pages = [&](const Place& c) {
-    const int* row = p.table + (long long)c.b * p.ld_table;
-#pragma unroll
-    for (int s = 0; s < TS; ++s) {
-      const int t = c.j * TILE + 16 * s;
-      page[s] = t < c.len ? __ldg(row + (t >> p.c.log_page)) : 0;
+  // 32 entries of a sequence's row of the page table, one per lane
+  int pg = 0, pg_seq = -1, pg_first = 0;
+  auto page_of = [&](const Place& c, int t) {
+    const int i = t >> p.c.log_page;
+    if (c.b != pg_seq || (unsigned)(i - pg_first) >= 32u) {
+      pg_seq = c.b;
+      pg_first = i;
+      pg = i + lane <= (c.len - 1) >> p.c.log_page ? __ldg(p.table + (long long)c.b * p.ld_table + i + lane) : 0;
     }
+    return __shfl_sync(0xFFFFFFFFu, pg, i - pg_first);
   };
   auto copy_tile = [&](uint32_t stage) {
     const int head = in.u / p.blocks;
@@ -282,12 +324,13 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     for (int s = 0; s < TS; ++s) {
       const int t = in.j * TILE + 16 * s, rows = in.len - t;
       if (rows > 0) {
-        const bool ok = (unsigned)page[s] < (unsigned)p.c.n_pages;
+        const int entry = page_of(in, t);
+        const bool ok = (unsigned)entry < (unsigned)p.c.n_pages;
         if (!ok && lane == 0) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
-        const long long pg = ok ? page[s] : 0;
+        const long long page = ok ? entry : 0;
         const long long prow = (long long)head * p.c.page_size + (t & (p.c.page_size - 1));
-        const uint8_t* ks = p.c.k + pg * p.c.page_stride + prow * RB;
-        const uint8_t* vs = p.c.v + pg * p.c.page_stride + prow * RB;
+        const uint8_t* ks = p.c.k + page * p.c.page_stride + prow * RB;
+        const uint8_t* vs = p.c.v + page * p.c.page_stride + prow * RB;
 #pragma unroll
         for (int i = 0; i < RB / 32; ++i) {
           const int id = i * 32 + lane, row = id / (RB / 16), ch = id % (RB / 16);
@@ -298,7 +341,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         }
         if constexpr (L::QUANT) {
           if (lane < 4) {  // 16 scales of K, 16 of V
-            const __half* src = (lane & 2 ? p.c.vs : p.c.ks) + pg * p.c.scale_stride + prow + (lane & 1) * 8;
+            const __half* src = (lane & 2 ? p.c.vs : p.c.ks) + page * p.c.scale_stride + prow + (lane & 1) * 8;
             cp_async16(stage + 2 * L::SIDE + (lane & 2) * TILE + 32 * s + (lane & 1) * 16, src, ok ? 16 : 0);
           }
         }
@@ -313,67 +356,68 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   uint32_t qf[NT][DIM / 8];
   int from = 0;             // first tile of the current piece
   int done = 0;             // copies issued
-  if (n > 0) load_pages(in);
   auto issue = [&]() {
     if (done < n) {
       copy_tile(ring_a + (done % p.stages) * L::STAGE);
       advance<TILE>(p, units, in);
-      if (done + 1 < n) load_pages(in);
     }
     ++done;
     cp_commit();
   };
+  int h0 = 0, gn = 0;       // the unit's first query head, and their number
+  auto begin_piece = [&]() {
+    const int head = at.u / p.blocks, blk = at.u - head * p.blocks;
+    h0 = head * p.group + blk * 8 * NT;
+    gn = min(8 * NT, p.group - blk * 8 * NT);
+    // the unit's query heads as B fragments, columns past them zero
+    from = at.j;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[a][nt][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) psum[nt][e] = 0.f;
+      const bool live = nt * 8 + rho < gn;
+      const __nv_bfloat16* qr = p.q + at.b * p.ld_q + (long long)(h0 + nt * 8 + rho) * DIM;
+      constexpr int QB = KIND == SPEAR_KV_BF16 ? 8 : KIND == SPEAR_KV_INT8 ? 16 : (DIM >= 128 ? 32 : 16);
+      // lane c holds dims [4 QB i + QB c, + QB) for each i
+#pragma unroll
+      for (int i8 = 0; i8 < DIM / 32; ++i8) {
+        const int d = (i8 / (QB / 8)) * 4 * QB + QB * cl + (i8 % (QB / 8)) * 8;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (live) w = __ldg(reinterpret_cast<const uint4*>(qr + d));
+        uint32_t* f = qf[nt] + 4 * i8;
+        if constexpr (KIND == SPEAR_KV_BF16) {
+          f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
+        } else if constexpr (KIND == SPEAR_KV_INT8) {  // bytes 0, 2 and 1, 3 of a word
+          f[0] = __byte_perm(w.x, w.y, 0x5410), f[1] = __byte_perm(w.x, w.y, 0x7632);
+          f[2] = __byte_perm(w.z, w.w, 0x5410), f[3] = __byte_perm(w.z, w.w, 0x7632);
+        } else {  // nibbles i and i + 4 of a word
+          f[0] = __byte_perm(w.x, w.z, 0x5410), f[1] = __byte_perm(w.x, w.z, 0x7632);
+          f[2] = __byte_perm(w.y, w.w, 0x5410), f[3] = __byte_perm(w.y, w.w, 0x7632);
+        }
+      }
+      if constexpr (KIND == SPEAR_KV_INT4) {
+        const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        float sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < DIM / 8; k += 2) mma_bf16_16816(sq, ones, qf[nt][k], qf[nt][k + 1]);
+        kfix[nt][0] = -kInt4Offset * sq[0];
+        kfix[nt][1] = -kInt4Offset * sq[1];
+      }
+    }
+  };
   for (int i = 0; i < p.stages - 1; ++i) issue();
+  if (n > 0) begin_piece();  // its loads are under way with the first copies
   for (int i = 0; i < n; ++i) {
     cp_wait(p.stages - 2);
     __syncwarp();  // tile i is in, and every lane is through with tile i - 1
     issue();
     const uint32_t st = ring_a + (i % p.stages) * L::STAGE;
-    const int head = at.u / p.blocks, blk = at.u - head * p.blocks;
-    const int h0 = head * p.group + blk * 8 * NT, gn = min(8 * NT, p.group - blk * 8 * NT);
-    if (i == 0 || at.j == 0) {
-      // a new piece: the unit's query heads as B fragments, columns past them zero
-      from = at.j;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-        for (int a = 0; a < MT; ++a)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[a][nt][e] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) psum[nt][e] = 0.f;
-        const bool live = nt * 8 + rho < gn;
-        const __nv_bfloat16* qr = p.q + at.b * p.ld_q + (long long)(h0 + nt * 8 + rho) * DIM;
-        constexpr int QB = KIND == SPEAR_KV_BF16 ? 8 : KIND == SPEAR_KV_INT8 ? 16 : (DIM >= 128 ? 32 : 16);
-        // lane c holds dims [4 QB i + QB c, + QB) for each i
-#pragma unroll
-        for (int i8 = 0; i8 < DIM / 32; ++i8) {
-          const int d = (i8 / (QB / 8)) * 4 * QB + QB * cl + (i8 % (QB / 8)) * 8;
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (live) w = __ldg(reinterpret_cast<const uint4*>(qr + d));
-          uint32_t* f = qf[nt] + 4 * i8;
-          if constexpr (KIND == SPEAR_KV_BF16) {
-            f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
-          } else if constexpr (KIND == SPEAR_KV_INT8) {  // bytes 0, 2 and 1, 3 of a word
-            f[0] = __byte_perm(w.x, w.y, 0x5410), f[1] = __byte_perm(w.x, w.y, 0x7632);
-            f[2] = __byte_perm(w.z, w.w, 0x5410), f[3] = __byte_perm(w.z, w.w, 0x7632);
-          } else {  // nibbles i and i + 4 of a word
-            f[0] = __byte_perm(w.x, w.z, 0x5410), f[1] = __byte_perm(w.x, w.z, 0x7632);
-            f[2] = __byte_perm(w.y, w.w, 0x5410), f[3] = __byte_perm(w.y, w.w, 0x7632);
-          }
-        }
-        if constexpr (KIND == SPEAR_KV_INT4) {
-          const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-          float sq[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < DIM / 8; k += 2) mma_bf16_16816(sq, ones, qf[nt][k], qf[nt][k + 1]);
-          kfix[nt][0] = -kInt4Offset * sq[0];
-          kfix[nt][1] = -kInt4Offset * sq[1];
-        }
-      }
-    }
     // ---- scores: S[token][head] ---------------------------------------------------------
     const int rows = at.len - at.j * TILE;  // live tokens from the tile's first on
     float s[TS][NT][4];
@@ -616,17 +660,22 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         pieces[2 * warp + (unit_ends ? 0 : 1)] = {t0 + i - at.j, at.nt, at.b * units + at.u, from, at.j + 1};
     }
     advance<TILE>(p, units, at);
+    if (unit_ends && i + 1 < n) begin_piece();
   }
   cp_wait(0);
   __syncthreads();
 
-  // ---- join the pieces of each unit ---------------------------------------------------------------
-  auto piece_at = [&](int i) -> float* {
-    uint8_t* r = smem + (size_t)(i >> 1) * (ring_bytes + p.piece * 4);
-    return reinterpret_cast<float*>(i & 1 ? r : r + ring_bytes);
-  };
-  // value of element (h, d) over pieces at(0..count), with the common maximum and sum
-  auto finish = [&](const Piece& pc, int count, auto global, auto at_piece, float* part) {
+  // ---- join the pieces of each unit -----------------------------------------------------------
+  constexpr int CH = (DIM + 127) / 128;      // 128-value parts of a head: one per warp and step
+  constexpr int LD = DIM >= 128 ? 128 : DIM;  // values of such a part
+  // Joins part `item` (head, part) of a unit's pieces at(0..count): their common
+  // maximum and sum, and LD values of the output, one float4 per lane.
+  auto join = [&](int unit, int count, int item, auto global, auto at_piece, float* part) {
+    const int u = unit % units, b = unit / units;
+    const int head = u / p.blocks, blk = u - head * p.blocks;
+    const int first = head * p.group + blk * 8 * NT, num = min(8 * NT, p.group - blk * 8 * NT);
+    const int h = item / CH, d = (item % CH) * 128 + 4 * lane;
+    if (h >= num || 4 * lane >= LD) return;
     // pieces of other CTAs are read past this SM's L1
     auto get = [](const float* f) {
       if constexpr (decltype(global)::value) return __ldcg(f);
@@ -636,79 +685,110 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       if constexpr (decltype(global)::value) return __ldcg(reinterpret_cast<const float4*>(f));
       else return *reinterpret_cast<const float4*>(f);
     };
-    const int u = pc.unit % units, b = pc.unit / units;
-    const int head = u / p.blocks, blk = u - head * p.blocks;
-    const int h0 = head * p.group + blk * 8 * NT, gn = min(8 * NT, p.group - blk * 8 * NT);
-    for (int i = tid; i < gn * (DIM / 4); i += W * 32) {
-      const int h = i / (DIM / 4), d = (i % (DIM / 4)) * 4;
-      float mx = -INFINITY, sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < count; ++k) mx = fmaxf(mx, get(at_piece(k) + gn * DIM + h));
-#pragma unroll 4
-      for (int k = 0; k < count; ++k) {
-        const float* f = at_piece(k);
-        const float w = exp2_(get(f + gn * DIM + h) - mx);
-        const float4 v = get4(f + h * DIM + d);
-        sum = fmaf(w, get(f + gn * DIM + gn + h), sum);
-        o.x = fmaf(w, v.x, o.x);
-        o.y = fmaf(w, v.y, o.y);
-        o.z = fmaf(w, v.z, o.z);
-        o.w = fmaf(w, v.w, o.w);
-      }
-      if (part) {
-        __stcg(reinterpret_cast<float4*>(part + h * DIM + d), o);
-        if (d == 0) {
-          __stcg(part + gn * DIM + h, mx);
-          __stcg(part + gn * DIM + gn + h, sum);
+    float mx = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int STEP = 8;  // pieces in flight
+    for (int k0 = 0; k0 < count; k0 += STEP) {
+      float pm[STEP], pl[STEP];
+      float4 pv[STEP];
+#pragma unroll
+      for (int k = 0; k < STEP; ++k) {
+        pm[k] = -INFINITY;
+        pl[k] = 0.f;
+        pv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k < count) {
+          const float* f = at_piece(k0 + k);
+          pm[k] = get(f + num * DIM + h);
+          pl[k] = get(f + num * DIM + num + h);
+          pv[k] = get4(f + h * DIM + d);
         }
-      } else {
-        const float inv = 1.f / sum;
-        *reinterpret_cast<uint2*>(p.out + b * p.ld_out + (long long)(h0 + h) * DIM + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (p.lse && d == 0) p.lse[(long long)b * p.heads + h0 + h] = (mx + log2f(sum)) * 0.6931471805599453f;
       }
+      float top = mx;
+#pragma unroll
+      for (int k = 0; k < STEP; ++k) top = fmaxf(top, pm[k]);
+      const float w0 = mx == -INFINITY ? 0.f : exp2_(mx - top);
+      mx = top;
+      sum *= w0;
+      o.x *= w0, o.y *= w0, o.z *= w0, o.w *= w0;
+#pragma unroll
+      for (int k = 0; k < STEP; ++k)
+        if (k0 + k < count) {
+          const float w = exp2_(pm[k] - mx);
+          sum = fmaf(w, pl[k], sum);
+          o.x = fmaf(w, pv[k].x, o.x);
+          o.y = fmaf(w, pv[k].y, o.y);
+          o.z = fmaf(w, pv[k].z, o.z);
+          o.w = fmaf(w, pv[k].w, o.w);
+        }
+    }
+    if (part) {
+      __stcg(reinterpret_cast<float4*>(part + h * DIM + d), o);
+      if (d == 0) {
+        __stcg(part + num * DIM + h, mx);
+        __stcg(part + num * DIM + num + h, sum);
+      }
+    } else {
+      const float inv = 1.f / sum;
+      *reinterpret_cast<uint2*>(p.out + b * p.ld_out + (long long)(first + h) * DIM + d) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (p.lse && d == 0) p.lse[(long long)b * p.heads + first + h] = (mx + log2f(sum)) * 0.6931471805599453f;
     }
   };
-  if (tid == 0) {
-    int k = 0;
-    for (int i = 0; i < 2 * W; ++i)
-      if (pieces[i].unit >= 0) order[k++] = i;
-    for (; k < 2 * W; ++k) order[k] = -1;
-    joins[0] = joins[1] = 0;
+  // Lane i of every warp looks at piece i; a unit's pieces are neighbours among those
+  // that are there.  heads: the first piece of each unit.
+  const int mine_unit = lane < 2 * W ? pieces[lane].unit : -1;
+  const unsigned there = __ballot_sync(0xFFFFFFFFu, mine_unit >= 0);
+  const unsigned below = there & ((1u << lane) - 1u);
+  const int prev_unit = __shfl_sync(0xFFFFFFFFu, mine_unit, below ? 31 - __clz(below) : 0);
+  unsigned heads = __ballot_sync(0xFFFFFFFFu, mine_unit >= 0 && (!below || prev_unit != mine_unit));
+  const int items = min(p.group, 8 * NT) * CH;
+  int open[2] = {-1, -1};  // first pieces of the units that come from another CTA, go on in one
+  for (int at_item = warp; heads; heads &= heads - 1) {
+    const int k = __ffs(heads) - 1;
+    const unsigned later = heads & (heads - 1);
+    const unsigned set = there & ~((1u << k) - 1u) & (later ? (1u << (__ffs(later) - 1)) - 1u : ~0u);
+    const int last = 31 - __clz(set);
+    const bool starts = pieces[k].from == 0, ends = pieces[last].to == pieces[k].nt;
+    float* part = nullptr;
+    if (!(starts && ends)) {
+      open[starts] = k;
+      part = p.parts + ((size_t)blockIdx.x * 2 + starts) * p.piece;
+    }
+    // the items of all units are dealt to the warps in turn
+    for (; at_item < items; at_item += W)
+      join(
+          pieces[k].unit, __popc(set), at_item, std::false_type{},
+          [&, rest = set](int) mutable {  // asked for in order
+            const int e = __ffs(rest) - 1;
+            rest &= rest - 1;
+            uint8_t* r = smem + (size_t)(e >> 1) * (ring_bytes + p.piece * 4);
+            return reinterpret_cast<const float*>(e & 1 ? r : r + ring_bytes);
+          },
+          part);
+    at_item -= items;
   }
-  __syncthreads();
-  Piece open[2];
-  open[0].unit = open[1].unit = -1;
-  for (int k = 0; k < 2 * W && order[k] >= 0;) {
-    const Piece pc = pieces[order[k]];
-    int e = k + 1;
-    while (e < 2 * W && order[e] >= 0 && pieces[order[e]].unit == pc.unit) ++e;
-    const bool starts = pc.from == 0, ends = pieces[order[e - 1]].to == pc.nt;
-    const int side = starts ? 1 : 0;  // its place among the CTA's parts, if it is open
-    float* part = starts && ends ? nullptr : p.parts + ((size_t)blockIdx.x * 2 + side) * p.piece;
-    finish(pc, e - k, std::false_type{}, [&](int i) { return piece_at(order[k + i]); }, part);
-    if (part) open[side] = pc;
-    k = e;
-  }
-  if (open[0].unit < 0 && open[1].unit < 0) return;
+  if (open[0] < 0 && open[1] < 0) return;
   __threadfence();
   __syncthreads();
-  if (tid == 0) {
-    for (int side = 0; side < 2; ++side)
-      if (open[side].unit >= 0) {
-        const int c0 = split.owner(open[side].start) / W, c1 = split.owner(open[side].start + open[side].nt - 1) / W;
-        joins[side] = atomicAdd(p.tickets + c0, 1) == c1 - c0;
-        if (joins[side]) p.tickets[c0] = 0;
+  int c0[2], c1[2];  // the CTAs that the open units span
+  for (int side = 0; side < 2; ++side)
+    if (open[side] >= 0) {
+      const Piece& pc = pieces[open[side]];
+      c0[side] = cut.owner(pc.start);
+      c1[side] = cut.owner(pc.start + pc.nt - 1);
+      if (tid == side) {
+        joins[side] = atomicAdd(p.tickets + c0[side], 1) == c1[side] - c0[side];
+        if (joins[side]) p.tickets[c0[side]] = 0;
+        __threadfence();
       }
-    __threadfence();
-  }
+    }
   __syncthreads();
   for (int side = 0; side < 2; ++side)
-    if (joins[side]) {
-      const int c0 = split.owner(open[side].start) / W, c1 = split.owner(open[side].start + open[side].nt - 1) / W;
-      finish(open[side], c1 - c0 + 1, std::true_type{},
-             [&](int i) { return p.parts + ((size_t)(c0 + i) * 2 + (i == 0)) * p.piece; }, nullptr);
-    }
+    if (joins[side])
+      for (int item = warp; item < items; item += W)
+        join(
+            pieces[open[side]].unit, c1[side] - c0[side] + 1, item, std::true_type{},
+            [&](int i) { return p.parts + ((size_t)(c0[side] + i) * 2 + (i == 0)) * p.piece; }, nullptr);
 }
 
 // ---------------------------------------------------------------------------
@@ -766,7 +846,9 @@ static cudaError_t launch_attn(AttnArgs& a, const AttnPlan& pl, cudaStream_t st)
   // no more CTAs than the longest possible line gives work to
   const long long tiles = (long long)a.c.heads * a.blocks * a.n_seqs * ((a.max_len + L::TILE - 1) / L::TILE);
   const long long need = (tiles + (long long)kMinTiles * W - 1) / ((long long)kMinTiles * W);
-  const int grid = (int)(need < pl.ctas ? need : pl.ctas);
+  const long long all_units = (long long)a.c.heads * a.blocks * a.n_seqs;
+  const long long most = need > all_units ? need : all_units;
+  const int grid = (int)(most < pl.ctas ? most : pl.ctas);
   k<<<grid, W * 32, smem, st>>>(a);
   return cudaGetLastError();
 }
