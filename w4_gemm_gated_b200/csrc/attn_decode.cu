@@ -148,17 +148,20 @@ __device__ __forceinline__ int clamp_len(const AttnArgs& p, int b) {
   return n < 0 ? 0 : min(n, p.max_len);
 }
 
-// A place on the line of tiles.
+// A place on the line of tiles: sequence, kv head, block of its query heads,
+// tile of the unit.
 struct Place {
-  int b, u, j, nt, len;
+  int b, head, blk, j, nt, len;
 };
 
 template <int TILE>
-__device__ __forceinline__ void advance(const AttnArgs& p, int units, Place& c) {
+__device__ __forceinline__ void advance(const AttnArgs& p, Place& c) {
   if (++c.j < c.nt) return;
   c.j = 0;
-  if (++c.u < units) return;
-  c.u = 0;
+  if (++c.blk < p.blocks) return;
+  c.blk = 0;
+  if (++c.head < p.c.heads) return;
+  c.head = 0;
   do {
     if (++c.b >= p.n_seqs) return;
     c.len = clamp_len(p, c.b);
@@ -278,8 +281,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     c.len = clamp_len(p, lo);
     c.nt = (int)(before[lo + 1] - before[lo]);
     const long long r = t - before[lo] * units;
-    c.u = (int)quotient(r, c.nt);
-    c.j = (int)(r - (long long)c.u * c.nt);
+    const int u = (int)quotient(r, c.nt);
+    c.head = u / p.blocks;
+    c.blk = u - c.head * p.blocks;
+    c.j = (int)(r - (long long)u * c.nt);
     return c;
   };
   const Cut cut(total, ctas);
@@ -318,32 +323,46 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     }
     return __shfl_sync(0xFFFFFFFFu, pg, i - pg_first);
   };
+  // A lane's chunk of a block's first 512 bytes; the next 512 bytes lie STEP rows on.
+  constexpr int CPR = RB / 16, STEP = 32 / CPR;
+  const int c_row = lane / CPR, c_ch = lane % CPR;
+  const uint32_t k_dst = c_row * RB + ((c_ch ^ L::xk(c_row)) << 4);
+  const uint32_t v_dst = c_row * RB + ((c_ch ^ L::xv(c_row)) << 4) + L::SIDE;
+  const uint8_t* k_src = p.c.k + lane * 16;
+  const uint8_t* v_src = p.c.v + lane * 16;
+  // lanes 0 to 3: 8 scales each, of K, K, V, V
+  const __half* s_src = L::QUANT ? (lane & 2 ? p.c.vs : p.c.ks) + (lane & 1) * 8 : nullptr;
+  const uint32_t s_dst = 2 * L::SIDE + (lane & 2) * TILE + (lane & 1) * 16;
   auto copy_tile = [&](uint32_t stage) {
-    const int head = in.u / p.blocks;
+    const int t0 = in.j * TILE;
 #pragma unroll
     for (int s = 0; s < TS; ++s) {
-      const int t = in.j * TILE + 16 * s, rows = in.len - t;
+      const int t = t0 + 16 * s, rows = in.len - t;
       if (rows > 0) {
         const int entry = page_of(in, t);
         const bool ok = (unsigned)entry < (unsigned)p.c.n_pages;
-        if (!ok && lane == 0) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
-        const long long page = ok ? entry : 0;
-        const long long prow = (long long)head * p.c.page_size + (t & (p.c.page_size - 1));
-        const uint8_t* ks = p.c.k + page * p.c.page_stride + prow * RB;
-        const uint8_t* vs = p.c.v + page * p.c.page_stride + prow * RB;
+        const int row = (in.head << p.c.log_page) + (t & (p.c.page_size - 1));  // in the page
+        const uint32_t page = ok ? entry : 0;
+        const long long at_row = ((long long)((unsigned long long)page * p.c.page_step) << 4) + (long long)row * RB;
+        const uint32_t d = stage + 16 * s * RB;
+        if (ok && rows >= 16) {
 #pragma unroll
-        for (int i = 0; i < RB / 32; ++i) {
-          const int id = i * 32 + lane, row = id / (RB / 16), ch = id % (RB / 16);
-          const int bytes = ok && row < rows ? 16 : 0;
-          const uint32_t d = stage + (16 * s + row) * RB;
-          cp_async16(d + ((ch ^ L::xk(row)) << 4), ks + id * 16, bytes);
-          cp_async16(d + L::SIDE + ((ch ^ L::xv(row)) << 4), vs + id * 16, bytes);
+          for (int i = 0; i < RB / 32; ++i) {
+            cp_async16(d + (k_dst ^ (L::xk(i * STEP) << 4)) + i * 512, k_src + at_row + i * 512, 16);
+            cp_async16(d + (v_dst ^ (L::xv(i * STEP) << 4)) + i * 512, v_src + at_row + i * 512, 16);
+          }
+        } else {  // rows past the end, and pages that are none, are zeros
+          if (!ok && lane == 0) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
+#pragma unroll
+          for (int i = 0; i < RB / 32; ++i) {
+            const int bytes = ok && c_row + i * STEP < rows ? 16 : 0;
+            cp_async16(d + (k_dst ^ (L::xk(i * STEP) << 4)) + i * 512, k_src + at_row + i * 512, bytes);
+            cp_async16(d + (v_dst ^ (L::xv(i * STEP) << 4)) + i * 512, v_src + at_row + i * 512, bytes);
+          }
         }
         if constexpr (L::QUANT) {
-          if (lane < 4) {  // 16 scales of K, 16 of V
-            const __half* src = (lane & 2 ? p.c.vs : p.c.ks) + page * p.c.scale_stride + prow + (lane & 1) * 8;
-            cp_async16(stage + 2 * L::SIDE + (lane & 2) * TILE + 32 * s + (lane & 1) * 16, src, ok ? 16 : 0);
-          }
+          if (lane < 4)
+            cp_async16(stage + s_dst + 32 * s, s_src + ((unsigned long long)page * p.c.scale_step << 3) + row, ok ? 16 : 0);
         }
       }
     }
@@ -355,20 +374,22 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   float kfix[NT][2];        // int4: -136 sum of q
   uint32_t qf[NT][DIM / 8];
   int from = 0;             // first tile of the current piece
-  int done = 0;             // copies issued
+  int done = 0;             // tiles whose copies are under way
+  uint32_t put = ring_a, take = ring_a;  // the stages of the next tile to copy, to work on
+  const uint32_t ring_end = ring_a + ring_bytes;
   auto issue = [&]() {
     if (done < n) {
-      copy_tile(ring_a + (done % p.stages) * L::STAGE);
-      advance<TILE>(p, units, in);
+      copy_tile(put);
+      put = put + L::STAGE == ring_end ? ring_a : put + L::STAGE;
+      advance<TILE>(p, in);
     }
     ++done;
     cp_commit();
   };
   int h0 = 0, gn = 0;       // the unit's first query head, and their number
   auto begin_piece = [&]() {
-    const int head = at.u / p.blocks, blk = at.u - head * p.blocks;
-    h0 = head * p.group + blk * 8 * NT;
-    gn = min(8 * NT, p.group - blk * 8 * NT);
+    h0 = at.head * p.group + at.blk * 8 * NT;
+    gn = min(8 * NT, p.group - at.blk * 8 * NT);
     // the unit's query heads as B fragments, columns past them zero
     from = at.j;
 #pragma unroll
@@ -417,7 +438,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     cp_wait(p.stages - 2);
     __syncwarp();  // tile i is in, and every lane is through with tile i - 1
     issue();
-    const uint32_t st = ring_a + (i % p.stages) * L::STAGE;
+    const uint32_t st = take;
+    take = take + L::STAGE == ring_end ? ring_a : take + L::STAGE;
     // ---- scores: S[token][head] ---------------------------------------------------------
     const int rows = at.len - at.j * TILE;  // live tokens from the tile's first on
     float s[TS][NT][4];
@@ -478,15 +500,26 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
           f0 *= lds_half(sa + 2 * r0);
           f1 *= lds_half(sa + 2 * r1);
         }
-        const bool ok0 = 16 * b + r0 < rows, ok1 = 16 * b + r1 < rows;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[b][nt][e] = ok0 ? s[b][nt][e] * f0 : -INFINITY;
-            s[b][nt][e + 2] = ok1 ? s[b][nt][e + 2] * f1 : -INFINITY;
-            top[nt][e] = fmaxf(top[nt][e], fmaxf(s[b][nt][e], s[b][nt][e + 2]));
+            s[b][nt][e] *= f0;
+            s[b][nt][e + 2] *= f1;
           }
+        if (16 * b + 16 > rows) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (16 * b + r0 >= rows) s[b][nt][e] = -INFINITY;
+              if (16 * b + r1 >= rows) s[b][nt][e + 2] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[b][nt][e], s[b][nt][e + 2]));
       }
     }
     // ---- running maximum; what is there is scaled down where it grew -----------------------
@@ -523,13 +556,15 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     for (int b = 0; b < TS; ++b) {
       if (16 * b < rows) {
         const int r0 = L::tok(rho), r1 = L::tok(rho + 8);
-        const bool ok0 = 16 * b + r0 < rows, ok1 = 16 * b + r1 < rows;
         float f0 = 1.f, f1 = 1.f;
         if constexpr (L::QUANT) {
-          // scales of rows past the end may be anything
           const uint32_t sa = st + 2 * L::SIDE + 2 * TILE + 32 * b;
-          f0 = ok0 ? lds_half(sa + 2 * r0) : 0.f;
-          f1 = ok1 ? lds_half(sa + 2 * r1) : 0.f;
+          f0 = lds_half(sa + 2 * r0);
+          f1 = lds_half(sa + 2 * r1);
+          if (16 * b + 16 > rows) {  // scales of rows past the end may be anything
+            if (16 * b + r0 >= rows) f0 = 0.f;
+            if (16 * b + r1 >= rows) f1 = 0.f;
+          }
         }
         uint32_t pb[NT][2];
 #pragma unroll
@@ -657,9 +692,9 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
           }
         }
       if (!whole && lane == 0)
-        pieces[2 * warp + (unit_ends ? 0 : 1)] = {t0 + i - at.j, at.nt, at.b * units + at.u, from, at.j + 1};
+        pieces[2 * warp + (unit_ends ? 0 : 1)] = {t0 + i - at.j, at.nt, at.b * units + at.head * p.blocks + at.blk, from, at.j + 1};
     }
-    advance<TILE>(p, units, at);
+    advance<TILE>(p, at);
     if (unit_ends && i + 1 < n) begin_piece();
   }
   cp_wait(0);

@@ -34,6 +34,8 @@ int check_kv_cache(const spear_kv_cache* c, KvView* out) {
   if (quant && c->scale_stride != 0 && (c->scale_stride < page_scales || c->scale_stride % 8))
     return set_error(SPEAR_ERR_INVALID_ARG, "scale_stride=%lld: 0, or a multiple of 8 of at least %lld",
                      c->scale_stride, page_scales);
+  if (c->page_stride >> 36 || c->scale_stride >> 35)
+    return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "pages lie more than 2^36 bytes apart");
   out->kind = c->kind;
   out->n_pages = c->n_pages;
   out->page_size = c->page_size;
@@ -46,6 +48,8 @@ int check_kv_cache(const spear_kv_cache* c, KvView* out) {
   out->vs = quant ? reinterpret_cast<__half*>(c->v_scales) : nullptr;
   out->page_stride = c->page_stride ? c->page_stride : (long long)page_bytes;
   out->scale_stride = c->scale_stride ? c->scale_stride : page_scales;
+  out->page_step = (uint32_t)(out->page_stride / 16);
+  out->scale_step = (uint32_t)(out->scale_stride / 8);
   return SPEAR_OK;
 }
 

@@ -16,6 +16,7 @@ struct KvView {
   __half* ks;
   __half* vs;
   long long page_stride, scale_stride;  // bytes, elements
+  uint32_t page_step, scale_step;       // the same in 16 bytes
 };
 
 // Bits of a stored value.
