@@ -44,62 +44,69 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return s;
 }
 
-// V vectors of 8 values per thread: vector j * blockDim.x + threadIdx.x of the row.
+// V vectors of 8 values per thread: vector j * blockDim.x + threadIdx.x of the
+// row.  All of a row's loads go out before the first sum.
 template <int V>
-__global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs p) {
+__global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant__ NormArgs p) {
   __shared__ float red[2][32];
   const long long row = blockIdx.x, base = row * p.K;
   const int nv = p.K / 8;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint4 xw[V], yw[V], gw[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = j * blockDim.x + threadIdx.x;
+    xw[j] = yw[j] = gw[j] = none;
+    if (i < nv) {
+      if (p.y) yw[j] = *reinterpret_cast<const uint4*>(p.y + base + 8 * i);
+      xw[j] = *reinterpret_cast<const uint4*>(p.x + base + 8 * i);
+      if (p.gate) gw[j] = __ldg(reinterpret_cast<const uint4*>(p.gate + row * p.gate_ld + 8 * i));
+    }
+  }
   float x[V][8];
   if (p.y) {
-    float u[V][8];
-    float sq = 0.f;
+    float r = 1.f;
+    if (p.post) {
+      float sq = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int i = j * blockDim.x + threadIdx.x;
-      if (i < nv) {
-        unpack8(*reinterpret_cast<const uint4*>(p.y + base + 8 * i), u[j]);
-        unpack8(*reinterpret_cast<const uint4*>(p.x + base + 8 * i), x[j]);
+      for (int j = 0; j < V; ++j) {
+        float u[8];
+        unpack8(yw[j], u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq += u[j][e] * u[j][e];
+        for (int e = 0; e < 8; ++e) sq = fmaf(u[e], u[e], sq);
       }
+      r = rsqrtf(block_sum(sq, red[0]) / p.K + p.eps);
     }
-    const float r = p.post ? rsqrtf(block_sum(sq, red[0]) / p.K + p.eps) : 1.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int i = j * blockDim.x + threadIdx.x;
-      if (i < nv) {
-        if (p.post) {
-          float w[8];
-          unpack8(*reinterpret_cast<const uint4*>(p.post + 8 * i), w);
+      float u[8], w[8];
+      unpack8(yw[j], u);
+      if (p.post) {
+        unpack8(i < nv ? __ldg(reinterpret_cast<const uint4*>(p.post + 8 * i)) : none, w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[j][e] *= r * w[e];
-        }
-        if (p.gate) {
-          float w[8];
-          unpack8(*reinterpret_cast<const uint4*>(p.gate + row * p.gate_ld + 8 * i), w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[j][e] *= w[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[j][e] = fmaf(p.b, u[j][e], p.a * x[j][e]);
-        if (p.x_out) *reinterpret_cast<uint4*>(p.x_out + base + 8 * i) = pack8(x[j]);
+        for (int e = 0; e < 8; ++e) u[e] *= r * w[e];
       }
+      if (p.gate) {
+        unpack8(gw[j], w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] *= w[e];
+      }
+      unpack8(xw[j], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[j][e] = fmaf(p.b, u[e], p.a * w[e]);
+      if (p.x_out && i < nv) *reinterpret_cast<uint4*>(p.x_out + base + 8 * i) = pack8(x[j]);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int i = j * blockDim.x + threadIdx.x;
-      if (i < nv) unpack8(*reinterpret_cast<const uint4*>(p.x + base + 8 * i), x[j]);
-    }
+    for (int j = 0; j < V; ++j) unpack8(xw[j], x[j]);
   }
   if (!p.h) return;
   float sq = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j)
-    if (j * blockDim.x + threadIdx.x < nv)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sq += x[j][e] * x[j][e];
+    for (int e = 0; e < 8; ++e) sq = fmaf(x[j][e], x[j][e], sq);
   const float r = rsqrtf(block_sum(sq, red[1]) / p.K + p.eps);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -107,7 +114,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs p) {
     if (i < nv) {
       if (p.pre) {
         float w[8];
-        unpack8(*reinterpret_cast<const uint4*>(p.pre + 8 * i), w);
+        unpack8(__ldg(reinterpret_cast<const uint4*>(p.pre + 8 * i)), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[j][e] *= r * w[e];
       } else {
@@ -117,6 +124,12 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs p) {
       *reinterpret_cast<uint4*>(p.h + base + 8 * i) = pack8(x[j]);
     }
   }
+}
+
+template <int V>
+static void launch_norm(const NormArgs& a, int M, cudaStream_t st) {
+  const int threads = ((a.K / 8 + V - 1) / V + 31) / 32 * 32;
+  block_norm_kernel<V><<<M, threads, 0, st>>>(a);
 }
 
 }  // namespace spear
@@ -156,10 +169,13 @@ extern "C" int spear_block_norm(const uint16_t* x, const uint16_t* y, int M, int
   const NormArgs a = {bf(x), bf(y), bf(post_weight), bf(gate), bf(pre_weight),
                       reinterpret_cast<__nv_bfloat16*>(x_out), reinterpret_cast<__nv_bfloat16*>(h), gate_ld, K,
                       residual_scale, block_scale, eps};
-  const int nv = K / 8;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int threads = ((nv + 1) / 2 + 31) / 32 * 32;
-  block_norm_kernel<2><<<M, threads, 0, st>>>(a);
+  // one vector per thread while a row has an SM to itself, where the chain from the
+  // loads to the stores counts (4096 wide: 2.4 us against 2.7 with two for one row,
+  // 3.9 against 4.3 for 256); two beyond, whose loads in flight HBM needs (8192
+  // rows: 53.6 us, 61.8 with one, 55.7 with four)
+  if (K <= 8192 && M <= 4 * device_sm_count()) launch_norm<1>(a, M, st);
+  else launch_norm<2>(a, M, st);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SPEAR_OK : set_cuda_error("block norm launch", e);
 }
