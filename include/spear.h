@@ -252,7 +252,7 @@ typedef struct spear_kv_cache {
   /* Distance of consecutive pages, for pages that lie inside a larger
    * allocation (K and V of a page side by side, pages of several layers):
    * bytes for k and v, elements for the scales.  Multiples of 16 bytes, at
-   * least a page; 0 = pages lie back to back. */
+   * least a page, under 2^36 bytes; 0 = pages lie back to back. */
   long long page_stride;
   long long scale_stride;
 } spear_kv_cache;
@@ -304,7 +304,8 @@ int spear_kv_read(const spear_kv_cache* cache, const int* slots, int n, uint16_t
  * A length outside its range is cut to it and a page number outside the cache
  * leaves its tokens' keys and values zero; both are reported as
  * SPEAR_ERR_DEVICE_CHECK (spear_read_status), and the sequence's results are
- * then unspecified.  0 <= n_seqs <= 4096 (0: nothing is launched).  The result does not depend on
+ * then unspecified.  0 <= n_seqs <= 4096 (0: nothing is launched);
+ * n_seqs * max_pages * page_size * n_q_heads < 2^35.  The result does not depend on
  * timing: the split over the cache is a function of the lengths alone. */
 size_t spear_attn_workspace_bytes(const spear_kv_cache* cache, int n_q_heads);
 int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q, long long ld_q, int n_seqs, int n_q_heads,

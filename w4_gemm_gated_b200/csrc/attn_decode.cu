@@ -48,7 +48,6 @@ struct AttnArgs {
   long long ld_q, ld_out;
   int ld_table, max_len, n_seqs, heads, group;
   int blocks;   // units per kv head: ceil(group / (8 NT))
-  int stages;   // ring stages per warp
   int piece;    // floats of a piece: heads of a unit x (DIM + 2)
   float scale;  // times log2(e)
   WsHeader* hdr;
@@ -63,15 +62,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Wait until at most n of this thread's copy groups are in flight.
-__device__ __forceinline__ void cp_wait(int n) {
-  if (n <= 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (n == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else asm volatile("cp.async.wait_group 4;" ::: "memory");
+// Wait until at most N of this thread's copy groups are in flight.
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-constexpr int kMaxStages = 6;
 
 template <int N>
 __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
@@ -171,126 +166,161 @@ __device__ __forceinline__ void advance(const AttnArgs& p, Place& c) {
 
 // A warp's unfinished part of a unit.
 struct Piece {
-  long long start;  // the unit's first tile on the line
-  int nt;           // its tiles
-  int unit;         // b * units + u; -1: no piece
-  int from, to;     // tiles [from, to)
+  unsigned start;  // the unit's first tile on the line
+  int nt;          // its tiles
+  int unit;        // (sequence, kv head, block) numbered through; -1: no piece
+  int from, to;    // tiles [from, to)
 };
-
-// a / b for a >= 0, b > 0 (the 64-bit division takes several times as long)
-__device__ __forceinline__ long long quotient(long long a, int b) {
-  return (unsigned long long)a >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
-}
 
 // `total` tiles cut into `parts` runs of q or q + 1.
 struct Cut {
-  long long q;
-  int more;  // the first `more` runs are one longer
-  __device__ __forceinline__ Cut(long long total, int parts) {
-    q = quotient(total, parts);
-    more = (int)(total - q * parts);
-  }
-  __device__ __forceinline__ long long begin(int w) const { return q * w + min(w, more); }
-  __device__ __forceinline__ int owner(long long t) const {  // q > 0
-    const long long border = (q + 1) * more;
-    // q + 1 fits an int wherever a run does
-    return (int)(t < border ? quotient(t, (int)q + 1) : more + quotient(t - border, (int)q));
+  unsigned q, more;  // the first `more` runs are one longer
+  __device__ __forceinline__ Cut(unsigned total, unsigned parts) : q(total / parts), more(total - q * parts) {}
+  __device__ __forceinline__ unsigned begin(unsigned w) const { return q * w + min(w, more); }
+  __device__ __forceinline__ int owner(unsigned t) const {  // q > 0
+    const unsigned border = (q + 1) * more;
+    return t < border ? t / (q + 1) : more + (t - border) / q;
   }
 };
+
+constexpr int attn_warps(int kind, int dim) { return kind == SPEAR_KV_BF16 && dim == 256 ? 4 : 8; }
+constexpr int attn_per_sm(int kind, int dim, int nt) { return kind != SPEAR_KV_BF16 && dim < 256 && nt == 1 ? 2 : 1; }
+
+// Shared memory of a CTA: per warp a ring of stages and the place of a first
+// piece.  227 KB per SM less 1 KB that each CTA takes besides, and 1 KB for the
+// kernel's static arrays.
+template <int KIND, int DIM, int NT>
+struct Room {
+  using L = Lay<KIND, DIM>;
+  static constexpr int W = attn_warps(KIND, DIM), PER_SM = attn_per_sm(KIND, DIM, NT);
+  static constexpr int PIECE = (8 * NT * (DIM + 2) + 3) / 4 * 4;  // floats: output, maximum, sum of each head
+  static constexpr int ROOM = (227 * 1024 / PER_SM - 2048) / W - PIECE * 4;
+  static constexpr int STAGES = ROOM / L::STAGE < 6 ? ROOM / L::STAGE : 6;
+  static constexpr int RING = STAGES * L::STAGE;
+  static constexpr int BYTES = W * (RING + PIECE * 4);
+  static_assert(STAGES >= 2 && RING >= PIECE * 4, "a last piece takes the ring's place");
+};
+
+constexpr int kMaxSeqs = 4096;
 
 template <int KIND, int DIM, int NT, int W, int PER_SM>
 __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_constant__ AttnArgs p) {
   using L = Lay<KIND, DIM>;
+  using R = Room<KIND, DIM, NT>;
+  static_assert(R::BYTES >= 4 * (kMaxSeqs + 1), "the line lies in the rings' place");
   constexpr int TILE = L::TILE, TS = L::TS, RB = L::RB, MT = DIM / 16;
+  constexpr unsigned ALL = 0xFFFFFFFFu;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long scan_sum[W];
+  __shared__ unsigned scan_sum[W];
   __shared__ int scan_max[W];
   __shared__ Piece pieces[2 * W];  // a warp's first (unit begun before it), its last
   __shared__ int joins[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rho = lane >> 2, cl = lane & 3;
   const int units = p.c.heads * p.blocks;
 
-  // ---- the line: tiles before each sequence --------------------------------------
-  long long* before = reinterpret_cast<long long*>(smem);  // n_seqs + 1 of them, in the rings' place
-  int longest = 0;                                         // tiles of the longest unit
+  // ---- the line: tiles before each sequence -----------------------------------------
+  // Up to 32 sequences: one per lane, in every warp alike.  More: in shared
+  // memory, in the rings' place, a run of `per` to each thread.
+  const bool few = p.n_seqs <= 32;
+  unsigned* before = reinterpret_cast<unsigned*>(smem);  // n_seqs + 1 of them
+  int len_l = 0, nt_l = 0;                               // few: this lane's sequence
+  unsigned before_l = 0, total;
+  int longest = 0;                                       // tiles of the longest unit
   {
-    const int per = (p.n_seqs + W * 32 - 1) / (W * 32);
-    const int b0 = tid * per, b1 = min(b0 + per, p.n_seqs);
-    long long sum = 0;
+    const int per = few ? 1 : (p.n_seqs + W * 32 - 1) / (W * 32);
+    const int b0 = few ? lane : tid * per, b1 = min(b0 + per, p.n_seqs);
+    unsigned sum = 0;
     for (int b = b0; b < b1; ++b) {
       const int n = __ldg(p.lens + b);
       if (blockIdx.x == 0 && (n < 0 || n > p.max_len)) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
-      const int nt = (min(max(n, 0), p.max_len) + TILE - 1) / TILE;
-      before[b] = nt;
-      sum += nt;
-      longest = max(longest, nt);
+      len_l = min(max(n, 0), p.max_len);
+      nt_l = (len_l + TILE - 1) / TILE;
+      if (!few) before[b] = nt_l;
+      sum += nt_l;
+      longest = max(longest, nt_l);
     }
-    long long inc = sum;
+    unsigned inc = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      const unsigned o = __shfl_up_sync(ALL, inc, d);
       if (lane >= d) inc += o;
     }
-    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-    if (lane == 31) scan_sum[warp] = inc, scan_max[warp] = longest;
+    longest = __reduce_max_sync(ALL, longest);
+    before_l = inc - sum;
+    total = __shfl_sync(ALL, inc, 31);
     if (lane < 2) pieces[2 * warp + lane].unit = -1;
     if (tid < 2) joins[tid] = 0;
-    __syncthreads();
-    long long off = inc - sum, all = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) off += scan_sum[w];
-      all += scan_sum[w];
-      longest = max(longest, scan_max[w]);
+    if (!few) {
+      if (lane == 31) scan_sum[warp] = inc, scan_max[warp] = longest;
+      __syncthreads();
+      unsigned off = before_l;
+      total = 0;
+      for (int w = 0; w < W; ++w) {
+        if (w < warp) off += scan_sum[w];
+        total += scan_sum[w];
+        longest = max(longest, scan_max[w]);
+      }
+      for (int b = b0; b < b1; ++b) {
+        const unsigned nt = before[b];
+        before[b] = off;
+        off += nt;
+      }
+      if (tid == 0) before[p.n_seqs] = total;
+      __syncthreads();
     }
-    for (int b = b0; b < b1; ++b) {
-      const long long nt = before[b];
-      before[b] = off;
-      off += nt;
-    }
-    if (tid == 0) before[p.n_seqs] = all;
-    __syncthreads();
   }
-  const long long total = before[p.n_seqs] * units;
+  total *= units;
   // sequences without tokens
   for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x)
-    if (before[b] == before[b + 1]) {
+    if (few ? __shfl_sync(ALL, nt_l, b) == 0 : before[b] == before[b + 1]) {
       for (int i = tid; i < p.heads * DIM / 8; i += W * 32)
         *reinterpret_cast<uint4*>(p.out + b * p.ld_out + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
       if (p.lse)
         for (int h = tid; h < p.heads; h += W * 32) p.lse[(long long)b * p.heads + h] = -INFINITY;
     }
-  // ---- this CTA's and this warp's run -----------------------------------------------
+  // ---- this CTA's and this warp's run ------------------------------------------------
   // Where no unit is longer than kShort tiles per warp of a CTA, CTAs take whole
   // units: the borders of even runs move on to the next unit's start.  A CTA
   // may then have up to kShort tiles per warp more than its share, which
   // costs no more than joining a unit across CTAs does, and saves that join.
   const bool aligned = longest <= kShort * W;
-  const int ctas = (int)(aligned ? min((long long)gridDim.x, min(total, (long long)p.n_seqs * units))
-                                 : min((long long)gridDim.x, quotient(total + kMinTiles * W - 1, kMinTiles * W)));
-  if ((int)blockIdx.x >= ctas) return;  // nothing for this CTA
-  auto place = [&](long long t) {       // of tile t < total
+  const unsigned ctas = min(gridDim.x, aligned ? min(total, (unsigned)(p.n_seqs * units))
+                                               : (total + kMinTiles * W - 1) / (kMinTiles * W));
+  if (blockIdx.x >= ctas) return;  // nothing for this CTA
+  auto place = [&](unsigned t) {   // of tile t < total, the same in every lane
     Place c;
-    int lo = 0, hi = p.n_seqs;  // before[lo] * units <= t < before[hi] * units
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (before[mid] * units <= t) lo = mid;
-      else hi = mid;
+    unsigned first;  // the sequence's first tile
+    if (few) {
+      c.b = 31 - __clz(__ballot_sync(ALL, nt_l > 0 && before_l * units <= t));
+      first = __shfl_sync(ALL, before_l, c.b) * units;
+      c.nt = __shfl_sync(ALL, nt_l, c.b);
+      c.len = __shfl_sync(ALL, len_l, c.b);
+    } else {
+      // the last b with before[b] * units <= t, 32 candidates at a time
+      int b = 0;
+      for (int step = p.n_seqs > 1024 ? 1024 : 32; step > 0; step >>= 5) {
+        const int i = b + lane * step;
+        b += step * (31 - __clz(__ballot_sync(ALL, i < p.n_seqs && before[i] * units <= t)));
+      }
+      c.b = b;
+      first = before[b] * units;
+      c.nt = before[b + 1] - before[b];
+      c.len = clamp_len(p, b);
     }
-    c.b = lo;
-    c.len = clamp_len(p, lo);
-    c.nt = (int)(before[lo + 1] - before[lo]);
-    const long long r = t - before[lo] * units;
-    const int u = (int)quotient(r, c.nt);
-    c.head = u / p.blocks;
-    c.blk = u - c.head * p.blocks;
-    c.j = (int)(r - (long long)u * c.nt);
+    const unsigned r = t - first, u = r / c.nt;
+    c.j = r - u * c.nt;
+    c.head = u;
+    c.blk = 0;
+    if (p.blocks > 1) {
+      c.head = u / p.blocks;
+      c.blk = u - c.head * p.blocks;
+    }
     return c;
   };
   const Cut cut(total, ctas);
-  long long c_begin = cut.begin(blockIdx.x), c_end = cut.begin(blockIdx.x + 1);
+  unsigned c_begin = cut.begin(blockIdx.x), c_end = cut.begin(blockIdx.x + 1);
   if (aligned) {
-    auto up = [&](long long t) {  // the next unit's start from t on
+    auto up = [&](unsigned t) {  // the next unit's start from t on
       if (t >= total) return total;
       const Place c = place(t);
       return c.j ? t + c.nt - c.j : t;
@@ -299,16 +329,15 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     c_end = up(c_end);
   }
   const Cut mine(c_end - c_begin, W);
-  const long long t0 = c_begin + mine.begin(warp);
-  const int n = (int)(mine.begin(warp + 1) - mine.begin(warp));
+  const unsigned t0 = c_begin + mine.begin(warp);
+  const int n = mine.begin(warp + 1) - mine.begin(warp);
   Place in = {};  // next tile to copy
   if (n > 0) in = place(t0);
   Place at = in;  // tile to work on
-  __syncthreads();  // the rings take over `before`'s place
+  if (!few) __syncthreads();  // the rings take over `before`'s place
 
-  const int ring_bytes = p.stages * L::STAGE;
-  uint8_t* ring = smem + (size_t)warp * (ring_bytes + p.piece * 4);
-  float* first_piece = reinterpret_cast<float*>(ring + ring_bytes);
+  uint8_t* ring = smem + (size_t)warp * (R::RING + R::PIECE * 4);
+  float* first_piece = reinterpret_cast<float*>(ring + R::RING);
   float* last_piece = reinterpret_cast<float*>(ring);  // once the run is through
   const uint32_t ring_a = smem_u32(ring);
 
@@ -333,38 +362,37 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   // lanes 0 to 3: 8 scales each, of K, K, V, V
   const __half* s_src = L::QUANT ? (lane & 2 ? p.c.vs : p.c.ks) + (lane & 1) * 8 : nullptr;
   const uint32_t s_dst = 2 * L::SIDE + (lane & 2) * TILE + (lane & 1) * 16;
+  auto copy_block = [&](uint32_t stage, int s, int t, int entry, int rows, auto whole) {
+    const bool ok = (unsigned)entry < (unsigned)p.c.n_pages;
+    const int row = (in.head << p.c.log_page) + (t & (p.c.page_size - 1));  // in the page
+    const uint32_t page = ok ? entry : 0;
+    const long long at_row = ((long long)((unsigned long long)page * p.c.page_step) << 4) + (long long)row * RB;
+    const uint32_t d = stage + 16 * s * RB;
+    // rows past the end, and pages that are none, are zeros
+    if (!ok && lane == 0) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
+    const int live = !ok ? 0 : decltype(whole)::value ? 16 : rows;
+#pragma unroll
+    for (int i = 0; i < RB / 32; ++i) {
+      const int bytes = (decltype(whole)::value ? live > 0 : c_row + i * STEP < live) ? 16 : 0;
+      cp_async16(d + (k_dst ^ (L::xk(i * STEP) << 4)) + i * 512, k_src + at_row + i * 512, bytes);
+      cp_async16(d + (v_dst ^ (L::xv(i * STEP) << 4)) + i * 512, v_src + at_row + i * 512, bytes);
+    }
+    if constexpr (L::QUANT) {
+      if (lane < 4)
+        cp_async16(stage + s_dst + 32 * s, s_src + ((unsigned long long)page * p.c.scale_step << 3) + row, ok ? 16 : 0);
+    }
+  };
   auto copy_tile = [&](uint32_t stage) {
-    const int t0 = in.j * TILE;
+    const int t = in.j * TILE, rows = in.len - t;
+    if (rows >= TILE) {
+      const int e0 = page_of(in, t);
 #pragma unroll
-    for (int s = 0; s < TS; ++s) {
-      const int t = t0 + 16 * s, rows = in.len - t;
-      if (rows > 0) {
-        const int entry = page_of(in, t);
-        const bool ok = (unsigned)entry < (unsigned)p.c.n_pages;
-        const int row = (in.head << p.c.log_page) + (t & (p.c.page_size - 1));  // in the page
-        const uint32_t page = ok ? entry : 0;
-        const long long at_row = ((long long)((unsigned long long)page * p.c.page_step) << 4) + (long long)row * RB;
-        const uint32_t d = stage + 16 * s * RB;
-        if (ok && rows >= 16) {
+      for (int s = 0; s < TS; ++s)
+        copy_block(stage, s, t + 16 * s, s && p.c.log_page == 4 ? page_of(in, t + 16 * s) : e0, 16, std::true_type{});
+    } else {
 #pragma unroll
-          for (int i = 0; i < RB / 32; ++i) {
-            cp_async16(d + (k_dst ^ (L::xk(i * STEP) << 4)) + i * 512, k_src + at_row + i * 512, 16);
-            cp_async16(d + (v_dst ^ (L::xv(i * STEP) << 4)) + i * 512, v_src + at_row + i * 512, 16);
-          }
-        } else {  // rows past the end, and pages that are none, are zeros
-          if (!ok && lane == 0) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
-#pragma unroll
-          for (int i = 0; i < RB / 32; ++i) {
-            const int bytes = ok && c_row + i * STEP < rows ? 16 : 0;
-            cp_async16(d + (k_dst ^ (L::xk(i * STEP) << 4)) + i * 512, k_src + at_row + i * 512, bytes);
-            cp_async16(d + (v_dst ^ (L::xv(i * STEP) << 4)) + i * 512, v_src + at_row + i * 512, bytes);
-          }
-        }
-        if constexpr (L::QUANT) {
-          if (lane < 4)
-            cp_async16(stage + s_dst + 32 * s, s_src + ((unsigned long long)page * p.c.scale_step << 3) + row, ok ? 16 : 0);
-        }
-      }
+      for (int s = 0; s < TS; ++s)
+        if (rows > 16 * s) copy_block(stage, s, t + 16 * s, page_of(in, t + 16 * s), rows - 16 * s, std::false_type{});
     }
   };
 
@@ -374,9 +402,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   float kfix[NT][2];        // int4: -136 sum of q
   uint32_t qf[NT][DIM / 8];
   int from = 0;             // first tile of the current piece
+  int h0 = 0, gn = 0;       // the unit's first query head, and their number
   int done = 0;             // tiles whose copies are under way
   uint32_t put = ring_a, take = ring_a;  // the stages of the next tile to copy, to work on
-  const uint32_t ring_end = ring_a + ring_bytes;
+  const uint32_t ring_end = ring_a + R::RING;
   auto issue = [&]() {
     if (done < n) {
       copy_tile(put);
@@ -386,11 +415,27 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     ++done;
     cp_commit();
   };
-  int h0 = 0, gn = 0;       // the unit's first query head, and their number
-  auto begin_piece = [&]() {
+  // A new piece: its query heads' values, columns past them zero ...
+  auto load_q = [&]() {
     h0 = at.head * p.group + at.blk * 8 * NT;
     gn = min(8 * NT, p.group - at.blk * 8 * NT);
-    // the unit's query heads as B fragments, columns past them zero
+    constexpr int QB = KIND == SPEAR_KV_BF16 ? 8 : KIND == SPEAR_KV_INT8 ? 16 : (DIM >= 128 ? 32 : 16);
+    // lane c holds dims [4 QB i + QB c, + QB) for each i
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const __nv_bfloat16* qr = p.q + at.b * p.ld_q + (long long)(h0 + nt * 8 + rho) * DIM;
+#pragma unroll
+      for (int i8 = 0; i8 < DIM / 32; ++i8) {
+        const int d = (i8 / (QB / 8)) * 4 * QB + QB * cl + (i8 % (QB / 8)) * 8;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (nt * 8 + rho < gn) w = __ldg(reinterpret_cast<const uint4*>(qr + d));
+        uint32_t* f = qf[nt] + 4 * i8;
+        f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
+      }
+    }
+  };
+  // ... as B fragments, in the order in which the codes' words come apart.
+  auto begin_piece = [&]() {
     from = at.j;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -402,24 +447,18 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         for (int e = 0; e < 4; ++e) acc[a][nt][e] = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) psum[nt][e] = 0.f;
-      const bool live = nt * 8 + rho < gn;
-      const __nv_bfloat16* qr = p.q + at.b * p.ld_q + (long long)(h0 + nt * 8 + rho) * DIM;
-      constexpr int QB = KIND == SPEAR_KV_BF16 ? 8 : KIND == SPEAR_KV_INT8 ? 16 : (DIM >= 128 ? 32 : 16);
-      // lane c holds dims [4 QB i + QB c, + QB) for each i
+      if constexpr (KIND != SPEAR_KV_BF16) {
 #pragma unroll
-      for (int i8 = 0; i8 < DIM / 32; ++i8) {
-        const int d = (i8 / (QB / 8)) * 4 * QB + QB * cl + (i8 % (QB / 8)) * 8;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (live) w = __ldg(reinterpret_cast<const uint4*>(qr + d));
-        uint32_t* f = qf[nt] + 4 * i8;
-        if constexpr (KIND == SPEAR_KV_BF16) {
-          f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
-        } else if constexpr (KIND == SPEAR_KV_INT8) {  // bytes 0, 2 and 1, 3 of a word
-          f[0] = __byte_perm(w.x, w.y, 0x5410), f[1] = __byte_perm(w.x, w.y, 0x7632);
-          f[2] = __byte_perm(w.z, w.w, 0x5410), f[3] = __byte_perm(w.z, w.w, 0x7632);
-        } else {  // nibbles i and i + 4 of a word
-          f[0] = __byte_perm(w.x, w.z, 0x5410), f[1] = __byte_perm(w.x, w.z, 0x7632);
-          f[2] = __byte_perm(w.y, w.w, 0x5410), f[3] = __byte_perm(w.y, w.w, 0x7632);
+        for (int i8 = 0; i8 < DIM / 32; ++i8) {
+          uint32_t* f = qf[nt] + 4 * i8;
+          const uint4 w = make_uint4(f[0], f[1], f[2], f[3]);
+          if constexpr (KIND == SPEAR_KV_INT8) {  // bytes 0, 2 and 1, 3 of a word
+            f[0] = __byte_perm(w.x, w.y, 0x5410), f[1] = __byte_perm(w.x, w.y, 0x7632);
+            f[2] = __byte_perm(w.z, w.w, 0x5410), f[3] = __byte_perm(w.z, w.w, 0x7632);
+          } else {  // nibbles i and i + 4 of a word
+            f[0] = __byte_perm(w.x, w.z, 0x5410), f[1] = __byte_perm(w.x, w.z, 0x7632);
+            f[2] = __byte_perm(w.y, w.w, 0x5410), f[3] = __byte_perm(w.y, w.w, 0x7632);
+          }
         }
       }
       if constexpr (KIND == SPEAR_KV_INT4) {
@@ -432,28 +471,22 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       }
     }
   };
-  for (int i = 0; i < p.stages - 1; ++i) issue();
-  if (n > 0) begin_piece();  // its loads are under way with the first copies
-  for (int i = 0; i < n; ++i) {
-    cp_wait(p.stages - 2);
-    __syncwarp();  // tile i is in, and every lane is through with tile i - 1
-    issue();
-    const uint32_t st = take;
-    take = take + L::STAGE == ring_end ? ring_a : take + L::STAGE;
-    // ---- scores: S[token][head] ---------------------------------------------------------
-    const int rows = at.len - at.j * TILE;  // live tokens from the tile's first on
+  // One tile; whole: every token of it is live.
+  const int r0 = L::tok(rho), r1 = L::tok(rho + 8);
+  auto work = [&](const uint32_t st, const int rows, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    // ---- scores: S[token][head] --------------------------------------------------------
     float s[TS][NT][4];
     float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
 #pragma unroll
     for (int b = 0; b < TS; ++b) {
-      if (16 * b < rows) {
+      if (WHOLE || 16 * b < rows) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[b][nt][e] = KIND == SPEAR_KV_INT4 ? kfix[nt][e & 1] : 0.f;
-        const int r0 = L::tok(rho), r1 = L::tok(rho + 8);
         const uint32_t ka = st + (16 * b + r0) * RB, kb = st + (16 * b + r1) * RB;
 #pragma unroll
         for (int i4 = 0; i4 < L::KI; ++i4) {
@@ -507,7 +540,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
             s[b][nt][e] *= f0;
             s[b][nt][e + 2] *= f1;
           }
-        if (16 * b + 16 > rows) {
+        if (!WHOLE) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -554,14 +587,13 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     // ---- weights, and O^T += V^T P -----------------------------------------------------------
 #pragma unroll
     for (int b = 0; b < TS; ++b) {
-      if (16 * b < rows) {
-        const int r0 = L::tok(rho), r1 = L::tok(rho + 8);
+      if (WHOLE || 16 * b < rows) {
         float f0 = 1.f, f1 = 1.f;
         if constexpr (L::QUANT) {
           const uint32_t sa = st + 2 * L::SIDE + 2 * TILE + 32 * b;
           f0 = lds_half(sa + 2 * r0);
           f1 = lds_half(sa + 2 * r1);
-          if (16 * b + 16 > rows) {  // scales of rows past the end may be anything
+          if (!WHOLE) {  // scales of rows past the end may be anything
             if (16 * b + r0 >= rows) f0 = 0.f;
             if (16 * b + r1 >= rows) f1 = 0.f;
           }
@@ -633,6 +665,20 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         }
       }
     }
+  };
+
+  if (n > 0) load_q();
+#pragma unroll 1
+  for (int i = 0; i < R::STAGES - 1; ++i) issue();
+  if (n > 0) begin_piece();
+  for (int i = 0; i < n; ++i) {
+    cp_wait<R::STAGES - 2>();
+    __syncwarp();  // tile i is in, and every lane is through with tile i - 1
+    issue();
+    const int rows = at.len - at.j * TILE;  // live tokens from the tile's first on
+    if (rows >= TILE) work(take, rows, std::true_type{});
+    else work(take, rows, std::false_type{});
+    take = take + L::STAGE == ring_end ? ring_a : take + L::STAGE;
     // ---- the end of the unit or of the run -----------------------------------------------------
     const bool unit_ends = at.j + 1 == at.nt;
     if (unit_ends || i + 1 == n) {
@@ -653,7 +699,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       const bool whole = unit_ends && from == 0;
       if (!unit_ends) {
         // every copy is in and read: the ring is this piece's place
-        cp_wait(0);
+        cp_wait<0>();
         __syncwarp();
       }
       float* dst = unit_ends ? first_piece : last_piece;
@@ -692,25 +738,31 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
           }
         }
       if (!whole && lane == 0)
-        pieces[2 * warp + (unit_ends ? 0 : 1)] = {t0 + i - at.j, at.nt, at.b * units + at.head * p.blocks + at.blk, from, at.j + 1};
+        pieces[2 * warp + (unit_ends ? 0 : 1)] = {t0 + i - at.j, at.nt, at.b * units + at.head * p.blocks + at.blk, from,
+                                                  at.j + 1};
     }
     advance<TILE>(p, at);
-    if (unit_ends && i + 1 < n) begin_piece();
+    if (unit_ends && i + 1 < n) {
+      load_q();
+      begin_piece();
+    }
   }
-  cp_wait(0);
+  cp_wait<0>();
   __syncthreads();
 
   // ---- join the pieces of each unit -----------------------------------------------------------
   constexpr int CH = (DIM + 127) / 128;      // 128-value parts of a head: one per warp and step
   constexpr int LD = DIM >= 128 ? 128 : DIM;  // values of such a part
-  // Joins part `item` (head, part) of a unit's pieces at(0..count): their common
-  // maximum and sum, and LD values of the output, one float4 per lane.
-  auto join = [&](int unit, int count, int item, auto global, auto at_piece, float* part) {
+  // Joins part `item` (head, part) of a unit's pieces: their common maximum and
+  // sum, and LD values of the output, one float4 per lane.  Lane k has piece k's
+  // maximum and sum (k0 + k's of many); set: the pieces that there are.
+  auto join = [&](int unit, int item, int count, unsigned set, auto global, auto piece_of, float* part) {
     const int u = unit % units, b = unit / units;
-    const int head = u / p.blocks, blk = u - head * p.blocks;
+    const int head = p.blocks > 1 ? u / p.blocks : u, blk = u - head * p.blocks;
     const int first = head * p.group + blk * 8 * NT, num = min(8 * NT, p.group - blk * 8 * NT);
     const int h = item / CH, d = (item % CH) * 128 + 4 * lane;
-    if (h >= num || 4 * lane >= LD) return;
+    if (h >= num) return;
+    const bool holds = 4 * lane < LD;
     // pieces of other CTAs are read past this SM's L1
     auto get = [](const float* f) {
       if constexpr (decltype(global)::value) return __ldcg(f);
@@ -722,40 +774,41 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     };
     float mx = -INFINITY, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int STEP = 8;  // pieces in flight
-    for (int k0 = 0; k0 < count; k0 += STEP) {
-      float pm[STEP], pl[STEP];
-      float4 pv[STEP];
-#pragma unroll
-      for (int k = 0; k < STEP; ++k) {
-        pm[k] = -INFINITY;
-        pl[k] = 0.f;
-        pv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + k < count) {
-          const float* f = at_piece(k0 + k);
-          pm[k] = get(f + num * DIM + h);
-          pl[k] = get(f + num * DIM + num + h);
-          pv[k] = get4(f + h * DIM + d);
-        }
+#pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += 32) {
+      if (decltype(global)::value) set = count - k0 >= 32 ? ALL : (1u << (count - k0)) - 1u;
+      float pm = -INFINITY, pl = 0.f;
+      if (set >> lane & 1) {
+        const float* f = piece_of(k0 + lane) + num * DIM + h;
+        pm = get(f);
+        pl = get(f + num);
       }
-      float top = mx;
+      float top = pm;
 #pragma unroll
-      for (int k = 0; k < STEP; ++k) top = fmaxf(top, pm[k]);
-      const float w0 = mx == -INFINITY ? 0.f : exp2_(mx - top);
+      for (int e = 16; e > 0; e >>= 1) top = fmaxf(top, __shfl_xor_sync(ALL, top, e));
+      top = fmaxf(top, mx);
+      const float keep = mx == -INFINITY ? 0.f : exp2_(mx - top);
+      const float w = set >> lane & 1 ? exp2_(pm - top) : 0.f;
       mx = top;
-      sum *= w0;
-      o.x *= w0, o.y *= w0, o.z *= w0, o.w *= w0;
+      pl *= w;
 #pragma unroll
-      for (int k = 0; k < STEP; ++k)
-        if (k0 + k < count) {
-          const float w = exp2_(pm[k] - mx);
-          sum = fmaf(w, pl[k], sum);
-          o.x = fmaf(w, pv[k].x, o.x);
-          o.y = fmaf(w, pv[k].y, o.y);
-          o.z = fmaf(w, pv[k].z, o.z);
-          o.w = fmaf(w, pv[k].w, o.w);
-        }
+      for (int e = 16; e > 0; e >>= 1) pl += __shfl_xor_sync(ALL, pl, e);
+      sum = sum * keep + pl;
+      o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+      const int base = k0;
+#pragma unroll 4
+      for (unsigned rest = set; rest; rest &= rest - 1) {
+        const int k = __ffs(rest) - 1;
+        const float wk = __shfl_sync(ALL, w, k);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (holds) v = get4(piece_of(base + k) + h * DIM + d);
+        o.x = fmaf(wk, v.x, o.x);
+        o.y = fmaf(wk, v.y, o.y);
+        o.z = fmaf(wk, v.z, o.z);
+        o.w = fmaf(wk, v.w, o.w);
+      }
     }
+    if (!holds) return;
     if (part) {
       __stcg(reinterpret_cast<float4*>(part + h * DIM + d), o);
       if (d == 0) {
@@ -792,12 +845,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     // the items of all units are dealt to the warps in turn
     for (; at_item < items; at_item += W)
       join(
-          pieces[k].unit, __popc(set), at_item, std::false_type{},
-          [&, rest = set](int) mutable {  // asked for in order
-            const int e = __ffs(rest) - 1;
-            rest &= rest - 1;
-            uint8_t* r = smem + (size_t)(e >> 1) * (ring_bytes + p.piece * 4);
-            return reinterpret_cast<const float*>(e & 1 ? r : r + ring_bytes);
+          pieces[k].unit, at_item, 32, set, std::false_type{},
+          [&](int e) {
+            uint8_t* r = smem + (size_t)(e >> 1) * (R::RING + R::PIECE * 4);
+            return reinterpret_cast<const float*>(e & 1 ? r : r + R::RING);
           },
           part);
     at_item -= items;
@@ -822,16 +873,13 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     if (joins[side])
       for (int item = warp; item < items; item += W)
         join(
-            pieces[open[side]].unit, c1[side] - c0[side] + 1, item, std::true_type{},
+            pieces[open[side]].unit, item, c1[side] - c0[side] + 1, 0u, std::true_type{},
             [&](int i) { return p.parts + ((size_t)(c0[side] + i) * 2 + (i == 0)) * p.piece; }, nullptr);
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-constexpr int attn_warps(int kind, int dim) { return kind == SPEAR_KV_BF16 && dim == 256 ? 4 : 8; }
-constexpr int attn_per_sm(int kind, int dim, int nt) { return kind != SPEAR_KV_BF16 && dim < 256 && nt == 1 ? 2 : 1; }
-
 struct AttnPlan {
   int nt, blocks, piece;
   int ctas;  // at most
@@ -857,34 +905,27 @@ static size_t attn_ws_bytes(const AttnPlan& a) {
 template <int KIND, int DIM, int NT>
 static cudaError_t launch_attn(AttnArgs& a, const AttnPlan& pl, cudaStream_t st) {
   using L = Lay<KIND, DIM>;
-  constexpr int W = attn_warps(KIND, DIM), PER_SM = attn_per_sm(KIND, DIM, NT);
-  // 227 KB per SM less 1 KB that each CTA takes besides, and 2 KB for the kernel's static arrays
-  constexpr size_t kRoom = PER_SM == 2 ? 227 * 512 - 1024 - 2048 : 227 * 1024 - 2048;
-  a.stages = (int)((kRoom / W - (size_t)a.piece * 4) / L::STAGE);
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  // at least two stages, whose place a piece takes over at the end
-  if (a.stages < 2 || (size_t)a.stages * L::STAGE < (size_t)a.piece * 4) return cudaErrorInvalidConfiguration;
-  size_t smem = (size_t)W * (a.stages * L::STAGE + (size_t)a.piece * 4);
-  const size_t line = sizeof(long long) * (a.n_seqs + 1);
-  if (smem < line) smem = line;
-  auto* k = attn_kernel<KIND, DIM, NT, W, PER_SM>;
+  using R = Room<KIND, DIM, NT>;
+  constexpr int W = R::W;
+  auto* k = attn_kernel<KIND, DIM, NT, W, R::PER_SM>;
   static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, R::BYTES);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   // no more CTAs than the longest possible line gives work to
   const long long tiles = (long long)a.c.heads * a.blocks * a.n_seqs * ((a.max_len + L::TILE - 1) / L::TILE);
+  if (tiles >> 31) return cudaErrorInvalidConfiguration;  // refused before
   const long long need = (tiles + (long long)kMinTiles * W - 1) / ((long long)kMinTiles * W);
   const long long all_units = (long long)a.c.heads * a.blocks * a.n_seqs;
   const long long most = need > all_units ? need : all_units;
   const int grid = (int)(most < pl.ctas ? most : pl.ctas);
-  k<<<grid, W * 32, smem, st>>>(a);
+  k<<<grid, W * 32, R::BYTES, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -910,7 +951,7 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   if (n_q_heads < 1 || n_q_heads > 1024 || n_q_heads % a.c.heads)
     return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "n_q_heads=%d: a multiple of the cache's %d heads, at most 1024",
                      n_q_heads, a.c.heads);
-  if (n_seqs < 0 || n_seqs > 4096) return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "n_seqs=%d: must be 0 to 4096", n_seqs);
+  if (n_seqs < 0 || n_seqs > kMaxSeqs) return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "n_seqs=%d: must be 0 to 4096", n_seqs);
   if (n_seqs == 0) return SPEAR_OK;
   if (!q || !page_table || !seq_lens || !out || !ws) return set_error(SPEAR_ERR_INVALID_ARG, "NULL pointer");
   if (!(fabsf(scale) < INFINITY)) return set_error(SPEAR_ERR_INVALID_ARG, "scale=%g: must be finite", scale);
@@ -919,6 +960,9 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
     return set_error(SPEAR_ERR_INVALID_ARG, "max_pages=%d ld_table=%d: 1 <= max_pages <= ld_table", max_pages, ld_table);
   if ((long long)max_pages * a.c.page_size > 0x7fff0000LL)
     return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "max_pages=%d: a sequence holds less than 2^31 - 2^16 tokens", max_pages);
+  if ((long long)n_seqs * max_pages * (a.c.page_size / 16) * n_q_heads >> 31)
+    return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE,
+                     "n_seqs=%d max_pages=%d: sequences x tokens x query heads must be under 2^35", n_seqs, max_pages);
   const long long row = (long long)n_q_heads * a.c.dim;
   if (ld_q < row || ld_out < row || ld_q % 8 || ld_out % 8)
     return set_error(SPEAR_ERR_INVALID_ARG, "ld_q=%lld ld_out=%lld: multiples of 8 of at least %lld", ld_q, ld_out, row);
