@@ -432,37 +432,30 @@ def make_kv_cache(kind: int, n_pages: int, page_size: int, n_heads: int, head_di
     return kv_cache_from_parts(k, v, ks, vs)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device index; torch.cuda.current_stream() costs 3 us
+# These calls take a few microseconds, of which the host's part is the longest
+# at a decode step's sizes.  The handle of a device's current stream, and the
+# current device, by torch's own short ways (torch.cuda.current_stream() takes 3 us).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
 
 
 def _launch(index: int, stream, tensors, fn, *args) -> None:
     """fn(*args, stream) on device `index`, whichever is current: on its current
-    stream, or on `stream`, whose use of the tensors the allocator is told.
-    These calls are short: the path with neither is kept straight."""
-    if stream is None:
-        if index == torch.cuda.current_device():
-            rc = fn(*args, _raw_stream(index))
-        else:
-            with torch.cuda.device(index):
-                rc = fn(*args, _raw_stream(index))
-    else:
+    stream, or on `stream`, whose use of the tensors the allocator is told."""
+    if stream is not None:
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-        with torch.cuda.device(index):
-            rc = fn(*args, stream.cuda_stream)
-    if rc != OK:
-        _check(rc)
+    with torch.cuda.device(index):
+        _check(fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream))
 
 
-def _new(like: torch.Tensor, stream, shape=None) -> torch.Tensor:
-    """A dense bf16 output on like's device, of its shape or `shape`, allocated on the stream that writes it."""
+def _new(stream, device, shape, strides) -> torch.Tensor:
+    """A bf16 output, allocated on the stream that writes it (empty_strided takes the least time to call)."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return _new(like, None, shape)
-    if shape is None:
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
-    return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+            return _new(None, device, shape, strides)
+    return torch.empty_strided(shape, strides, dtype=torch.bfloat16, device=device)
 
 
 def _rows(t: torch.Tensor, index: int, n: int, n_heads: int, head_dim: int, what: str) -> int:
@@ -490,7 +483,7 @@ def _i32(t: torch.Tensor, index: int, n: int, what: str) -> int:
 def _ws(t: torch.Tensor, index: int) -> tuple[int, int]:
     if t.get_device() != index or not t.is_contiguous():
         raise ValueError("the workspace must be contiguous, on the cache's device")
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, ws: torch.Tensor,
@@ -502,8 +495,13 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     ld_k, ld_v = _rows(k, di, n, G, D, "k"), _rows(v, di, n, G, D, "v")
     sp = _i32(slots, di, n, "slots")
     wp, wn = _ws(ws, di)
-    _launch(di, stream, (k, v, slots, ws, *cache.tensors), _kv_write, cache.ref, k.data_ptr(), ld_k, v.data_ptr(),
-            ld_v, sp, n, wp, wn)
+    args = cache.ref, k.data_ptr(), ld_k, v.data_ptr(), ld_v, sp, n, wp, wn
+    if stream is None and _current() == di:
+        rc = _kv_write(*args, _raw_stream(di))
+        if rc:
+            _check(rc)
+    else:
+        _launch(di, stream, (k, v, slots, ws, *cache.tensors), _kv_write, *args)
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, ws: torch.Tensor, k_out: torch.Tensor | None = None,
@@ -512,16 +510,22 @@ def kv_read(cache: KVCache, slots: torch.Tensor, ws: torch.Tensor, k_out: torch.
     n, di, G, D = slots.shape[0], cache.index, cache.n_heads, cache.head_dim
     sp = _i32(slots, di, n, "slots")
     wp, wn = _ws(ws, di)
+    shape, strides = (n, G, D), (G * D, D, 1)
     if k_out is None:
-        k_out = _new(slots, stream, (n, G, D))
+        k_out = _new(stream, cache.device, shape, strides)
     elif k_out.dtype is not torch.bfloat16 or _rows(k_out, di, n, G, D, "k_out") != G * D:
         raise ValueError("k_out must be contiguous bf16")
     if v_out is None:
-        v_out = _new(slots, stream, (n, G, D))
+        v_out = _new(stream, cache.device, shape, strides)
     elif v_out.dtype is not torch.bfloat16 or _rows(v_out, di, n, G, D, "v_out") != G * D:
         raise ValueError("v_out must be contiguous bf16")
-    _launch(di, stream, (slots, ws, k_out, v_out, *cache.tensors), _kv_read, cache.ref, sp, n, k_out.data_ptr(),
-            v_out.data_ptr(), wp, wn)
+    args = cache.ref, sp, n, k_out.data_ptr(), v_out.data_ptr(), wp, wn
+    if stream is None and _current() == di:
+        rc = _kv_read(*args, _raw_stream(di))
+        if rc:
+            _check(rc)
+    else:
+        _launch(di, stream, (slots, ws, k_out, v_out, *cache.tensors), _kv_read, *args)
     return k_out, v_out
 
 
@@ -554,7 +558,8 @@ def attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_l
     H = shape[1] if len(shape) == 3 else shape[1] // D
     ld_q = _rows(q, di, n, H, D, "q")
     if out is None:
-        out, ld_out = _new(q, stream), H * D
+        ld_out = H * D
+        out = _new(stream, cache.device, shape, (ld_out, D, 1) if len(shape) == 3 else (ld_out, 1))
     else:
         if out.shape != shape:
             raise ValueError("out must have q's shape")
@@ -569,10 +574,15 @@ def attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_l
                             or lse.get_device() != di):
         raise ValueError("lse must be contiguous fp32, n_seqs x n_q_heads, on the cache's device")
     wp, wn = _ws(ws, di)
-    _launch(di, stream, (q, out, page_table, seq_lens, lse, ws, *cache.tensors), _attn_decode, cache.ref, q.data_ptr(),
-            ld_q, n, H, page_table.data_ptr(), pages, t_strides[0] if n > 1 else pages, lp,
+    args = (cache.ref, q.data_ptr(), ld_q, n, H, page_table.data_ptr(), pages, t_strides[0] if n > 1 else pages, lp,
             D ** -0.5 if scale is None else scale, out.data_ptr(), ld_out, None if lse is None else lse.data_ptr(),
             wp, wn)
+    if stream is None and _current() == di:
+        rc = _attn_decode(*args, _raw_stream(di))
+        if rc:
+            _check(rc)
+    else:
+        _launch(di, stream, (q, out, page_table, seq_lens, lse, ws, *cache.tensors), _attn_decode, *args)
     return out
 
 
@@ -613,7 +623,7 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, pre_weight: to
     if x_out is not None:
         op = _norm_ptr(x_out, shape, di, "x_out")
     elif y is not None:
-        x_out = _new(x, stream)
+        x_out = _new(stream, x.device, shape, (K, 1))
         op = x_out.data_ptr()
     else:
         op = None
@@ -622,10 +632,15 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, pre_weight: to
     elif h is not None:
         hp = _norm_ptr(h, shape, di, "h")
     else:
-        h = _new(x, stream)
+        h = _new(stream, x.device, shape, (K, 1))
         hp = h.data_ptr()
-    _launch(di, stream, (x, y, pre_weight, post_weight, gate, x_out, h), _block_norm, xp, yp, M, K, post, gp, gate_ld,
-            residual_scale, block_scale, pre, eps, op, hp)
+    args = xp, yp, M, K, post, gp, gate_ld, residual_scale, block_scale, pre, eps, op, hp
+    if stream is None and _current() == di:
+        rc = _block_norm(*args, _raw_stream(di))
+        if rc:
+            _check(rc)
+    else:
+        _launch(di, stream, (x, y, pre_weight, post_weight, gate, x_out, h), _block_norm, *args)
     return (x if y is None else x_out), h
 
 
