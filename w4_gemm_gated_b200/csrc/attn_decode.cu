@@ -166,10 +166,10 @@ __device__ __forceinline__ void advance(const AttnArgs& p, Place& c) {
 
 // A warp's unfinished part of a unit.
 struct Piece {
-  unsigned start;  // the unit's first tile on the line
+  unsigned start;  // the unit's first tile on the line, which names the unit
   int nt;          // its tiles
-  int unit;        // (sequence, kv head, block) numbered through; -1: no piece
-  int from, to;    // tiles [from, to)
+  int from, to;    // tiles [from, to); to = 0: no piece
+  int b, h0, num;  // its sequence, its first query head and their number
 };
 
 // `total` tiles cut into `parts` runs of q or q + 1.
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     longest = __reduce_max_sync(ALL, longest);
     before_l = inc - sum;
     total = __shfl_sync(ALL, inc, 31);
-    if (lane < 2) pieces[2 * warp + lane].unit = -1;
+    if (lane < 2) pieces[2 * warp + lane].to = 0;
     if (tid < 2) joins[tid] = 0;
     if (!few) {
       if (lane == 31) scan_sum[warp] = inc, scan_max[warp] = longest;
@@ -738,8 +738,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
           }
         }
       if (!whole && lane == 0)
-        pieces[2 * warp + (unit_ends ? 0 : 1)] = {t0 + i - at.j, at.nt, at.b * units + at.head * p.blocks + at.blk, from,
-                                                  at.j + 1};
+        pieces[2 * warp + (unit_ends ? 0 : 1)] = {t0 + i - at.j, at.nt, from, at.j + 1, at.b, h0, gn};
     }
     advance<TILE>(p, at);
     if (unit_ends && i + 1 < n) {
@@ -753,82 +752,112 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   // ---- join the pieces of each unit -----------------------------------------------------------
   constexpr int CH = (DIM + 127) / 128;      // 128-value parts of a head: one per warp and step
   constexpr int LD = DIM >= 128 ? 128 : DIM;  // values of such a part
-  // Joins part `item` (head, part) of a unit's pieces: their common maximum and
-  // sum, and LD values of the output, one float4 per lane.  Lane k has piece k's
-  // maximum and sum (k0 + k's of many); set: the pieces that there are.
-  auto join = [&](int unit, int item, int count, unsigned set, auto global, auto piece_of, float* part) {
-    const int u = unit % units, b = unit / units;
-    const int head = p.blocks > 1 ? u / p.blocks : u, blk = u - head * p.blocks;
-    const int first = head * p.group + blk * 8 * NT, num = min(8 * NT, p.group - blk * 8 * NT);
+  // Part `item` (head, part) of a unit's pieces joined: their common maximum
+  // mx and sum, and LD values o of the output, one float4 per lane.  It goes to the
+  // output, or to `part` where pieces of other CTAs are still to come.
+  auto put_item = [&](const Piece& pc, int item, float mx, float sum, float4 o, float* part) {
     const int h = item / CH, d = (item % CH) * 128 + 4 * lane;
-    if (h >= num) return;
-    const bool holds = 4 * lane < LD;
-    // pieces of other CTAs are read past this SM's L1
-    auto get = [](const float* f) {
-      if constexpr (decltype(global)::value) return __ldcg(f);
-      else return *f;
-    };
-    auto get4 = [](const float* f) {
-      if constexpr (decltype(global)::value) return __ldcg(reinterpret_cast<const float4*>(f));
-      else return *reinterpret_cast<const float4*>(f);
-    };
-    float mx = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int k0 = 0; k0 < count; k0 += 32) {
-      if (decltype(global)::value) set = count - k0 >= 32 ? ALL : (1u << (count - k0)) - 1u;
-      float pm = -INFINITY, pl = 0.f;
-      if (set >> lane & 1) {
-        const float* f = piece_of(k0 + lane) + num * DIM + h;
-        pm = get(f);
-        pl = get(f + num);
-      }
-      float top = pm;
-#pragma unroll
-      for (int e = 16; e > 0; e >>= 1) top = fmaxf(top, __shfl_xor_sync(ALL, top, e));
-      top = fmaxf(top, mx);
-      const float keep = mx == -INFINITY ? 0.f : exp2_(mx - top);
-      const float w = set >> lane & 1 ? exp2_(pm - top) : 0.f;
-      mx = top;
-      pl *= w;
-#pragma unroll
-      for (int e = 16; e > 0; e >>= 1) pl += __shfl_xor_sync(ALL, pl, e);
-      sum = sum * keep + pl;
-      o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
-      const int base = k0;
-#pragma unroll 4
-      for (unsigned rest = set; rest; rest &= rest - 1) {
-        const int k = __ffs(rest) - 1;
-        const float wk = __shfl_sync(ALL, w, k);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (holds) v = get4(piece_of(base + k) + h * DIM + d);
-        o.x = fmaf(wk, v.x, o.x);
-        o.y = fmaf(wk, v.y, o.y);
-        o.z = fmaf(wk, v.z, o.z);
-        o.w = fmaf(wk, v.w, o.w);
-      }
-    }
-    if (!holds) return;
+    if (4 * lane >= LD) return;
     if (part) {
       __stcg(reinterpret_cast<float4*>(part + h * DIM + d), o);
       if (d == 0) {
-        __stcg(part + num * DIM + h, mx);
-        __stcg(part + num * DIM + num + h, sum);
+        __stcg(part + pc.num * DIM + h, mx);
+        __stcg(part + pc.num * DIM + pc.num + h, sum);
       }
     } else {
       const float inv = 1.f / sum;
-      *reinterpret_cast<uint2*>(p.out + b * p.ld_out + (long long)(first + h) * DIM + d) =
+      *reinterpret_cast<uint2*>(p.out + pc.b * p.ld_out + (long long)(pc.h0 + h) * DIM + d) =
           make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-      if (p.lse && d == 0) p.lse[(long long)b * p.heads + first + h] = (mx + log2f(sum)) * 0.6931471805599453f;
+      if (p.lse && d == 0) p.lse[(long long)pc.b * p.heads + pc.h0 + h] = (mx + log2f(sum)) * 0.6931471805599453f;
     }
+  };
+  // Pieces `set` of this CTA: lane k has piece k's maximum and sum.
+  auto join_here = [&](const Piece& pc, int item, unsigned set, float* part) {
+    const int h = item / CH, d = (item % CH) * 128 + 4 * lane;
+    if (h >= pc.num) return;
+    auto piece_of = [&](int e) {
+      uint8_t* r = smem + (size_t)(e >> 1) * (R::RING + R::PIECE * 4);
+      return reinterpret_cast<const float*>(e & 1 ? r : r + R::RING);
+    };
+    float pm = -INFINITY, w = 0.f, sum = 0.f;
+    const bool has = set >> lane & 1;
+    if (has) {
+      const float* f = piece_of(lane) + pc.num * DIM + h;
+      pm = f[0];
+      sum = f[pc.num];
+    }
+    float mx = pm;
+#pragma unroll
+    for (int e = 8; e > 0; e >>= 1) mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, e));  // 2 W <= 16 pieces
+    mx = __shfl_sync(ALL, mx, 0);
+    if (has) w = exp2_(pm - mx);
+    sum *= w;
+#pragma unroll
+    for (int e = 8; e > 0; e >>= 1) sum += __shfl_xor_sync(ALL, sum, e);
+    sum = __shfl_sync(ALL, sum, 0);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (; set; set &= set - 1) {
+      const int k = __ffs(set) - 1;
+      const float wk = __shfl_sync(ALL, w, k);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (4 * lane < LD) v = *reinterpret_cast<const float4*>(piece_of(k) + h * DIM + d);
+      o.x = fmaf(wk, v.x, o.x);
+      o.y = fmaf(wk, v.y, o.y);
+      o.z = fmaf(wk, v.z, o.z);
+      o.w = fmaf(wk, v.w, o.w);
+    }
+    put_item(pc, item, mx, sum, o, part);
+  };
+  // Parts of `count` CTAs from c0 on, read past this SM's L1, eight in flight.
+  auto join_parts = [&](const Piece& pc, int item, int first, int count) {
+    const int h = item / CH, d = (item % CH) * 128 + 4 * lane;
+    if (h >= pc.num) return;
+    constexpr int STEP = 8;
+    float mx = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += STEP) {
+      float pm[STEP], pl[STEP];
+      float4 pv[STEP];
+#pragma unroll
+      for (int k = 0; k < STEP; ++k) {
+        pm[k] = -INFINITY;
+        pl[k] = 0.f;
+        pv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k < count) {
+          // the unit's first CTA has it on its far side
+          const float* f = p.parts + ((size_t)(first + k0 + k) * 2 + (k0 + k == 0)) * p.piece;
+          pm[k] = __ldcg(f + pc.num * DIM + h);
+          pl[k] = __ldcg(f + pc.num * DIM + pc.num + h);
+          if (4 * lane < LD) pv[k] = __ldcg(reinterpret_cast<const float4*>(f + h * DIM + d));
+        }
+      }
+      float top = mx;
+#pragma unroll
+      for (int k = 0; k < STEP; ++k) top = fmaxf(top, pm[k]);
+      const float keep = mx == -INFINITY ? 0.f : exp2_(mx - top);
+      mx = top;
+      sum *= keep;
+      o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+      for (int k = 0; k < STEP; ++k) {
+        const float w = k0 + k < count ? exp2_(pm[k] - mx) : 0.f;
+        sum = fmaf(w, pl[k], sum);
+        o.x = fmaf(w, pv[k].x, o.x);
+        o.y = fmaf(w, pv[k].y, o.y);
+        o.z = fmaf(w, pv[k].z, o.z);
+        o.w = fmaf(w, pv[k].w, o.w);
+      }
+    }
+    put_item(pc, item, mx, sum, o, nullptr);
   };
   // Lane i of every warp looks at piece i; a unit's pieces are neighbours among those
   // that are there.  heads: the first piece of each unit.
-  const int mine_unit = lane < 2 * W ? pieces[lane].unit : -1;
-  const unsigned there = __ballot_sync(0xFFFFFFFFu, mine_unit >= 0);
-  const unsigned below = there & ((1u << lane) - 1u);
-  const int prev_unit = __shfl_sync(0xFFFFFFFFu, mine_unit, below ? 31 - __clz(below) : 0);
-  unsigned heads = __ballot_sync(0xFFFFFFFFu, mine_unit >= 0 && (!below || prev_unit != mine_unit));
+  const bool mine_there = lane < 2 * W && pieces[lane].to > 0;
+  const unsigned there = __ballot_sync(ALL, mine_there), below = there & ((1u << lane) - 1u);
+  unsigned heads =
+      __ballot_sync(ALL, mine_there && (!below || pieces[31 - __clz(below)].start != pieces[lane].start));
   const int items = min(p.group, 8 * NT) * CH;
   int open[2] = {-1, -1};  // first pieces of the units that come from another CTA, go on in one
   for (int at_item = warp; heads; heads &= heads - 1) {
@@ -843,38 +872,32 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       part = p.parts + ((size_t)blockIdx.x * 2 + starts) * p.piece;
     }
     // the items of all units are dealt to the warps in turn
-    for (; at_item < items; at_item += W)
-      join(
-          pieces[k].unit, at_item, 32, set, std::false_type{},
-          [&](int e) {
-            uint8_t* r = smem + (size_t)(e >> 1) * (R::RING + R::PIECE * 4);
-            return reinterpret_cast<const float*>(e & 1 ? r : r + R::RING);
-          },
-          part);
+    for (; at_item < items; at_item += W) join_here(pieces[k], at_item, set, part);
     at_item -= items;
   }
   if (open[0] < 0 && open[1] < 0) return;
-  __threadfence();
-  __syncthreads();
+  // The parts of every thread are ordered before the count by the barrier and its
+  // release, and read after its acquire by whoever counts last.
   int c0[2], c1[2];  // the CTAs that the open units span
   for (int side = 0; side < 2; ++side)
     if (open[side] >= 0) {
       const Piece& pc = pieces[open[side]];
       c0[side] = cut.owner(pc.start);
       c1[side] = cut.owner(pc.start + pc.nt - 1);
-      if (tid == side) {
-        joins[side] = atomicAdd(p.tickets + c0[side], 1) == c1[side] - c0[side];
-        if (joins[side]) p.tickets[c0[side]] = 0;
-        __threadfence();
-      }
     }
+  __syncthreads();
+  if (tid < 2 && open[tid] >= 0) {
+    int* ticket = p.tickets + c0[tid];
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
+    joins[tid] = old == c1[tid] - c0[tid];
+    if (joins[tid]) *ticket = 0;
+  }
   __syncthreads();
   for (int side = 0; side < 2; ++side)
     if (joins[side])
       for (int item = warp; item < items; item += W)
-        join(
-            pieces[open[side]].unit, item, c1[side] - c0[side] + 1, 0u, std::true_type{},
-            [&](int i) { return p.parts + ((size_t)(c0[side] + i) * 2 + (i == 0)) * p.piece; }, nullptr);
+        join_parts(pieces[open[side]], item, c0[side], c1[side] - c0[side] + 1);
 }
 
 // ---------------------------------------------------------------------------
