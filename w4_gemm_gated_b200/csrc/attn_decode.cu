@@ -56,7 +56,7 @@ struct AttnArgs {
 };
 
 constexpr int kMinTiles = 2;  // tiles a warp should have before more CTAs take part
-constexpr int kShort = 4;     // tiles per warp up to which a unit stays in one CTA
+constexpr int kShort = 32;    // tiles up to which a unit stays in one CTA
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -183,8 +183,13 @@ struct Cut {
   }
 };
 
-constexpr int attn_warps(int kind, int dim) { return kind == SPEAR_KV_BF16 && dim == 256 ? 4 : 8; }
-constexpr int attn_per_sm(int kind, int dim, int nt) { return kind != SPEAR_KV_BF16 && dim < 256 && nt == 1 ? 2 : 1; }
+// Warps of a CTA and CTAs of an SM.  Two CTAs, so that one streams while the other
+// starts or joins (bf16, 64 x 4096: one of 8 warps 108 us, two of 4 101, four of 2
+// 103).  Quantised kinds are bound by their arithmetic and take 16 warps where 128
+// registers do (two of 8; four of 4 cost more joins: 16 x 2048 int8 16.9 us, 18.6).
+constexpr bool attn_small(int kind, int dim, int nt) { return kind != SPEAR_KV_BF16 && dim < 256 && nt == 1; }
+constexpr int attn_warps(int kind, int dim, int nt) { return attn_small(kind, dim, nt) ? 8 : 4; }
+constexpr int attn_per_sm(int kind, int dim) { return kind == SPEAR_KV_BF16 && dim == 256 ? 1 : 2; }
 
 // Shared memory of a CTA: per warp a ring of stages and the place of a first
 // piece.  227 KB per SM less 1 KB that each CTA takes besides, and 1 KB for the
@@ -192,7 +197,7 @@ constexpr int attn_per_sm(int kind, int dim, int nt) { return kind != SPEAR_KV_B
 template <int KIND, int DIM, int NT>
 struct Room {
   using L = Lay<KIND, DIM>;
-  static constexpr int W = attn_warps(KIND, DIM), PER_SM = attn_per_sm(KIND, DIM, NT);
+  static constexpr int W = attn_warps(KIND, DIM, NT), PER_SM = attn_per_sm(KIND, DIM);
   static constexpr int PIECE = (8 * NT * (DIM + 2) + 3) / 4 * 4;  // floats: output, maximum, sum of each head
   static constexpr int ROOM = (227 * 1024 / PER_SM - 2048) / W - PIECE * 4;
   static constexpr int STAGES = ROOM / L::STAGE < 6 ? ROOM / L::STAGE : 6;
@@ -279,11 +284,11 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         for (int h = tid; h < p.heads; h += W * 32) p.lse[(long long)b * p.heads + h] = -INFINITY;
     }
   // ---- this CTA's and this warp's run ------------------------------------------------
-  // Where no unit is longer than kShort tiles per warp of a CTA, CTAs take whole
-  // units: the borders of even runs move on to the next unit's start.  A CTA
-  // may then have up to kShort tiles per warp more than its share, which
-  // costs no more than joining a unit across CTAs does, and saves that join.
-  const bool aligned = longest <= kShort * W;
+  // Where no unit is longer than kShort tiles, CTAs take whole units: the borders
+  // of even runs move on to the next unit's start.  A CTA may then have up to
+  // kShort tiles more than its share, which costs no more than joining a unit
+  // across CTAs does (97 tokens, 8 units: 7.4 us, 15.5 with joins), and saves that.
+  const bool aligned = longest <= kShort;
   const unsigned ctas = min(gridDim.x, aligned ? min(total, (unsigned)(p.n_seqs * units))
                                                : (total + kMinTiles * W - 1) / (kMinTiles * W));
   if (blockIdx.x >= ctas) return;  // nothing for this CTA
@@ -915,7 +920,7 @@ static AttnPlan plan_attn(const KvView& c, int n_q_heads) {
   a.blocks = (group + 8 * a.nt - 1) / (8 * a.nt);
   const int in_unit = group < 8 * a.nt ? group : 8 * a.nt;
   a.piece = (in_unit * (c.dim + 2) + 3) / 4 * 4;
-  a.ctas = device_sm_count() * attn_per_sm(c.kind, c.dim, a.nt);
+  a.ctas = device_sm_count() * attn_per_sm(c.kind, c.dim);
   return a;
 }
 
