@@ -18,8 +18,8 @@
 //
 // Arithmetic.  Tensor-core products over 16 tokens with the query heads as the 8
 // columns: S = K q (rows: tokens), then O^T += V^T P with P's layout turned by
-// movmatrix.  Running maximum, sum and output of a softmax in fp32, in powers of
-// two; the output is rescaled only when a maximum grows.  The weight times
+// movmatrix.  Running reference, sum and output of a softmax in fp32, in powers of
+// two; they are rescaled only when a score passes the reference.  The weight times
 // its value's scale is rounded to bf16 as the operand of the second product
 // (relative 2^-8 per weight, of the size of the output's own rounding); the sum
 // in the denominator is of the unrounded weights.  int8 codes become bf16
@@ -56,6 +56,7 @@ struct AttnArgs {
 };
 
 constexpr int kMinTiles = 2;  // tiles a warp should have before more CTAs take part
+constexpr float kSlack = 8.f;  // in powers of two
 constexpr int kShort = 32;    // tiles up to which a unit stays in one CTA
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -560,25 +561,26 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
           for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[b][nt][e], s[b][nt][e + 2]));
       }
     }
-    // ---- running maximum; what is there is scaled down where it grew -----------------------
-    bool grew = false;
+    // ---- the weights' reference m; what is there is scaled down where it moves -------------
+    // m follows the maximum only once a score lies more than kSlack above it: a
+    // weight of up to 2^kSlack does no harm in fp32 and bf16, and most tiles need
+    // neither the maximum over lanes nor new factors.
+    bool above = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xFFFFFFFFu, top[nt][e], d));
-        top[nt][e] = fmaxf(top[nt][e], m[nt][e]);
-        grew |= top[nt][e] > m[nt][e];
-      }
-    if (__any_sync(0xFFFFFFFFu, grew)) {
+      for (int e = 0; e < 2; ++e) above |= top[nt][e] > m[nt][e] + kSlack;
+    if (__any_sync(ALL, above)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          f[e] = m[nt][e] == -INFINITY ? 0.f : exp2_(m[nt][e] - top[nt][e]);
-          m[nt][e] = top[nt][e];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(ALL, top[nt][e], d));
+          const float now = fmaxf(top[nt][e], m[nt][e]);
+          f[e] = m[nt][e] == -INFINITY ? 0.f : exp2_(m[nt][e] - now);
+          m[nt][e] = now;
           l[nt][e] *= f[e];
         }
 #pragma unroll
@@ -589,6 +591,11 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         for (int e = 0; e < 4; ++e) psum[nt][e] *= f[e & 1];
       }
     }
+    float ref[NT][2];  // scores of -infinity alone leave m there: their weights are 0
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ref[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
     // ---- weights, and O^T += V^T P -----------------------------------------------------------
 #pragma unroll
     for (int b = 0; b < TS; ++b) {
@@ -608,7 +615,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         for (int nt = 0; nt < NT; ++nt) {
           float e[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) e[k] = exp2_(s[b][nt][k] - m[nt][k & 1]);
+          for (int k = 0; k < 4; ++k) e[k] = exp2_(s[b][nt][k] - ref[nt][k & 1]);
           l[nt][0] += e[0] + e[2];
           l[nt][1] += e[1] + e[3];
           pb[nt][0] = movmatrix(pack_bf16x2(e[0] * f0, e[1] * f0));
