@@ -1,4 +1,5 @@
-"""Build the CUDA library ``libspear.so`` in-tree for sm_100a.
+"""Build the CUDA library ``libspear.so`` in-tree for sm_100a, and the native
+marshalling module ``_bind`` of its binding (host code, against torch's headers).
 
 Usage: ``python -m w4_gemm_gated_b200.build [--force] [--verbose] [--checked]``.
 Objects go to ``_build/`` at the repository root; the shared library is
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspear.so")
 LIB_CHECKED = os.path.join(PKG, "libspear_checked.so")
+BIND = os.path.join(PKG, "_bind" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["api.cu", "pack.cu", "decode.cu", "decode2.cu", "decode3.cu", "ec.cu", "tc_gemm.cu", "noalloc.cu",
            "kv_cache.cu", "attn_decode.cu", "block_norm.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tma.cuh", "kv_cache.cuh"]
@@ -59,7 +62,33 @@ def _compile(src: str, verbose: bool, checked: bool = False) -> tuple[str, str]:
     return obj, log
 
 
+def build_bind(force: bool = False) -> str:
+    """The binding's native module; its CUDA side is reached through addresses
+    handed to it, so it links to torch alone."""
+    src, header = os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "spear.h")
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(os.path.getmtime(src),
+                                                                           os.path.getmtime(header)):
+        return BIND
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    includes = [os.path.join(ROOT, "include"), os.path.join(base, "include"),
+                os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+                sysconfig.get_paths()["include"]]
+    tmp = f"{BIND}.{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in includes], src,
+           "-o", tmp, "-L" + os.path.join(base, "lib"),
+           *["-l" + l for l in ("c10", "c10_cuda", "torch_cpu", "torch_cuda", "torch_python", "torch")]]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for bind.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
+    build_bind(force)
     lib = LIB_CHECKED if checked else LIB
     os.makedirs(os.path.join(BUILD, "checked") if checked else BUILD, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES]

@@ -21,6 +21,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), _LIB_NAME)
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with `python -m w4_gemm_gated_b200.build`")
 _lib = ctypes.CDLL(_LIB_PATH)
+from . import _bind  # noqa: E402  (native marshalling of the decoder-step calls, built beside the library)
 
 OK = 0
 ERR_INVALID_ARG = 1
@@ -370,8 +371,7 @@ class KVCache:
             self.k_scales.data_ptr() if quant else None, self.v_scales.data_ptr() if quant else None,
             self.k.stride(0) * self.k.element_size() if self.n_pages > 1 else 0,
             self.k_scales.stride(0) if quant and self.n_pages > 1 else 0)
-        self.ref = ctypes.byref(self.struct)
-        self.tensors = tuple(t for t in (self.k, self.v, self.k_scales, self.v_scales) if t is not None)
+        self.address = ctypes.addressof(self.struct)
 
 
 def _dense_pages(t: torch.Tensor) -> bool:
@@ -432,106 +432,23 @@ def make_kv_cache(kind: int, n_pages: int, page_size: int, n_heads: int, head_di
     return kv_cache_from_parts(k, v, ks, vs)
 
 
-# These calls take a few microseconds, of which the host's part is the longest
-# at a decode step's sizes.  The handle of a device's current stream, and the
-# current device, by torch's own short ways (torch.cuda.current_stream() takes 3 us).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current = torch._C._cuda_getDevice
-
-
-def _launch(index: int, stream, tensors, fn, *args) -> None:
-    """fn(*args, stream) on device `index`, whichever is current: on its current
-    stream, or on `stream`, whose use of the tensors the allocator is told."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-    with torch.cuda.device(index):
-        _check(fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream))
-
-
-def _new(stream, device, shape, strides) -> torch.Tensor:
-    """A bf16 output, allocated on the stream that writes it (empty_strided takes the least time to call)."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return _new(None, device, shape, strides)
-    return torch.empty_strided(shape, strides, dtype=torch.bfloat16, device=device)
-
-
-def _rows(t: torch.Tensor, index: int, n: int, n_heads: int, head_dim: int, what: str) -> int:
-    """Elements between the rows of t: n rows of n_heads x head_dim bf16 values (2-D or 3-D)."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{what} must be bf16")
-    shape, strides = t.shape, t.stride()
-    if len(shape) == 3:
-        ok = shape == (n, n_heads, head_dim) and strides[2] == 1 and (strides[1] == head_dim or n_heads == 1)
-    else:
-        ok = shape == (n, n_heads * head_dim) and strides[1] == 1
-    if not ok:
-        raise ValueError(f"{what} must be {n} rows of {n_heads} x {head_dim} consecutive values")
-    if t.get_device() != index:
-        raise ValueError(f"{what} must live on the cache's device")
-    return strides[0] if n > 1 else n_heads * head_dim
-
-
-def _i32(t: torch.Tensor, index: int, n: int, what: str) -> int:
-    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != index:
-        raise ValueError(f"{what} must be {n} contiguous int32 values on the cache's device")
-    return t.data_ptr()
-
-
-def _ws(t: torch.Tensor, index: int) -> tuple[int, int]:
-    if t.get_device() != index or not t.is_contiguous():
-        raise ValueError("the workspace must be contiguous, on the cache's device")
-    return t.data_ptr(), t.nbytes
-
-
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, ws: torch.Tensor,
              stream=None) -> None:
     """Write n new tokens' keys and values (n x n_heads x head_dim or n x (n_heads
     * head_dim) bf16; rows may be ranges of wider rows) at their slots (int32,
     page * page_size + offset; negative: skipped; no slot twice)."""
-    n, di, G, D = k.shape[0], cache.index, cache.n_heads, cache.head_dim
-    ld_k, ld_v = _rows(k, di, n, G, D, "k"), _rows(v, di, n, G, D, "v")
-    sp = _i32(slots, di, n, "slots")
-    wp, wn = _ws(ws, di)
-    args = cache.ref, k.data_ptr(), ld_k, v.data_ptr(), ld_v, sp, n, wp, wn
-    if stream is None and _current() == di:
-        rc = _kv_write(*args, _raw_stream(di))
-        if rc:
-            _check(rc)
-    else:
-        _launch(di, stream, (k, v, slots, ws, *cache.tensors), _kv_write, *args)
+    _bind.kv_write(cache.address, cache.index, k, v, slots, ws, stream)
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, ws: torch.Tensor, k_out: torch.Tensor | None = None,
             v_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The keys and values at n slots, n x n_heads x head_dim bf16 (a negative slot reads as zeros)."""
-    n, di, G, D = slots.shape[0], cache.index, cache.n_heads, cache.head_dim
-    sp = _i32(slots, di, n, "slots")
-    wp, wn = _ws(ws, di)
-    shape, strides = (n, G, D), (G * D, D, 1)
-    if k_out is None:
-        k_out = _new(stream, cache.device, shape, strides)
-    elif k_out.dtype is not torch.bfloat16 or _rows(k_out, di, n, G, D, "k_out") != G * D:
-        raise ValueError("k_out must be contiguous bf16")
-    if v_out is None:
-        v_out = _new(stream, cache.device, shape, strides)
-    elif v_out.dtype is not torch.bfloat16 or _rows(v_out, di, n, G, D, "v_out") != G * D:
-        raise ValueError("v_out must be contiguous bf16")
-    args = cache.ref, sp, n, k_out.data_ptr(), v_out.data_ptr(), wp, wn
-    if stream is None and _current() == di:
-        rc = _kv_read(*args, _raw_stream(di))
-        if rc:
-            _check(rc)
-    else:
-        _launch(di, stream, (slots, ws, k_out, v_out, *cache.tensors), _kv_read, *args)
-    return k_out, v_out
+    return _bind.kv_read(cache.address, cache.index, slots, ws, k_out, v_out, stream)
 
 
 def attn_workspace_bytes(cache: KVCache, n_q_heads: int) -> int:
     with torch.cuda.device(cache.index):
-        n = F["spear_attn_workspace_bytes"](cache.ref, n_q_heads)
+        n = F["spear_attn_workspace_bytes"](ctypes.byref(cache.struct), n_q_heads)
     if n == 0:
         raise SpearError(ERR_UNSUPPORTED_SHAPE, f"n_q_heads={n_q_heads} over a cache of {cache.n_heads} heads")
     return n
@@ -540,8 +457,9 @@ def attn_workspace_bytes(cache: KVCache, n_q_heads: int) -> int:
 def make_attn_workspace(cache: KVCache, n_q_heads: int, stream=None) -> torch.Tensor:
     """A workspace for attn_decode (any batch), kv_write and kv_read on this cache or others of its shape."""
     n = attn_workspace_bytes(cache, n_q_heads)
-    ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
-    _launch(cache.index, stream, (ws,), F["spear_workspace_init"], ws.data_ptr(), n)
+    with torch.cuda.device(cache.index), torch.cuda.stream(stream):
+        ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+        _check(F["spear_workspace_init"](_ptr(ws), n, _stream(None)))
     return ws
 
 
@@ -553,45 +471,7 @@ def attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_l
     rows may be ranges of wider rows; page_table: n_seqs x max_pages int32;
     seq_lens: int32; scale: 1 / sqrt(head_dim) if None; lse: optional fp32
     n_seqs x n_q_heads, written.  Returns out, of q's shape."""
-    shape, di, D = q.shape, cache.index, cache.head_dim
-    n = shape[0]
-    H = shape[1] if len(shape) == 3 else shape[1] // D
-    ld_q = _rows(q, di, n, H, D, "q")
-    if out is None:
-        ld_out = H * D
-        out = _new(stream, cache.device, shape, (ld_out, D, 1) if len(shape) == 3 else (ld_out, 1))
-    else:
-        if out.shape != shape:
-            raise ValueError("out must have q's shape")
-        ld_out = _rows(out, di, n, H, D, "out")
-    t_shape, t_strides = page_table.shape, page_table.stride()
-    if page_table.dtype is not torch.int32 or len(t_shape) != 2 or t_shape[0] != n \
-            or t_strides[1] != 1 and t_shape[1] > 1 or page_table.get_device() != di:
-        raise ValueError("page_table must be n_seqs x max_pages int32 with consecutive rows, on the cache's device")
-    pages = t_shape[1]
-    lp = _i32(seq_lens, di, n, "seq_lens")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, H) or not lse.is_contiguous()
-                            or lse.get_device() != di):
-        raise ValueError("lse must be contiguous fp32, n_seqs x n_q_heads, on the cache's device")
-    wp, wn = _ws(ws, di)
-    args = (cache.ref, q.data_ptr(), ld_q, n, H, page_table.data_ptr(), pages, t_strides[0] if n > 1 else pages, lp,
-            D ** -0.5 if scale is None else scale, out.data_ptr(), ld_out, None if lse is None else lse.data_ptr(),
-            wp, wn)
-    if stream is None and _current() == di:
-        rc = _attn_decode(*args, _raw_stream(di))
-        if rc:
-            _check(rc)
-    else:
-        _launch(di, stream, (q, out, page_table, seq_lens, lse, ws, *cache.tensors), _attn_decode, *args)
-    return out
-
-
-def _norm_ptr(t: torch.Tensor | None, shape, index: int, what: str) -> int | None:
-    if t is None:
-        return None
-    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
-        raise ValueError(f"{what} must be contiguous bf16 of shape {tuple(shape)}, on x's CUDA device")
-    return t.data_ptr()
+    return _bind.attn_decode(cache.address, cache.index, q, page_table, seq_lens, ws, scale, out, lse, stream)
 
 
 def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, pre_weight: torch.Tensor | None = None,
@@ -605,47 +485,12 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, pre_weight: to
     no y h = norm(x).  x, y: M x K bf16; weights K; gate K, 1 x K or M x K bf16 (rows
     may lie apart).  Returns (x_out, h), (x, h) without y; x_out=x updates x in
     place; norm=False leaves the norm out (after the last block) and returns (x_out, None)."""
-    shape, di = x.shape, x.get_device()
-    if len(shape) != 2 or di < 0:
-        raise ValueError("x must be M x K on a CUDA device")
-    M, K = shape
-    xp, yp = _norm_ptr(x, shape, di, "x"), _norm_ptr(y, shape, di, "y")
-    post, pre = _norm_ptr(post_weight, (K,), di, "post_weight"), _norm_ptr(pre_weight, (K,), di, "pre_weight")
-    gp, gate_ld = None, 0
-    if gate is not None:
-        g_shape, g_strides = gate.shape, gate.stride()
-        if gate.dtype is not torch.bfloat16 or g_shape not in ((K,), (1, K), (M, K)) or g_strides[-1] != 1 \
-                or gate.get_device() != di:
-            raise ValueError("gate must be bf16, K, 1 x K or M x K, with consecutive rows, on x's device")
-        gp = gate.data_ptr()
-        if len(g_shape) == 2 and g_shape[0] > 1:
-            gate_ld = g_strides[0]
-    if x_out is not None:
-        op = _norm_ptr(x_out, shape, di, "x_out")
-    elif y is not None:
-        x_out = _new(stream, x.device, shape, (K, 1))
-        op = x_out.data_ptr()
-    else:
-        op = None
-    if not norm:
-        h = hp = None
-    elif h is not None:
-        hp = _norm_ptr(h, shape, di, "h")
-    else:
-        h = _new(stream, x.device, shape, (K, 1))
-        hp = h.data_ptr()
-    args = xp, yp, M, K, post, gp, gate_ld, residual_scale, block_scale, pre, eps, op, hp
-    if stream is None and _current() == di:
-        rc = _block_norm(*args, _raw_stream(di))
-        if rc:
-            _check(rc)
-    else:
-        _launch(di, stream, (x, y, pre_weight, post_weight, gate, x_out, h), _block_norm, *args)
-    return (x if y is None else x_out), h
+    return _bind.block_norm(x, y, pre_weight, post_weight, gate, residual_scale, block_scale, eps, x_out, h, norm,
+                            stream)
 
 
-_kv_write, _kv_read = F["spear_kv_write"], F["spear_kv_read"]
-_attn_decode, _block_norm = F["spear_attn_decode"], F["spear_block_norm"]
+_bind.setup(*(ctypes.cast(F[name], _vp).value for name in ("spear_kv_write", "spear_kv_read", "spear_attn_decode",
+                                                           "spear_block_norm")), _check)
 
 
 def test_inject_timeout(kernel: int, wait_cycles: int = 0) -> None:
