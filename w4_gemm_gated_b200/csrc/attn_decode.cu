@@ -140,7 +140,7 @@ struct Lay {
 };
 
 __device__ __forceinline__ int clamp_len(const AttnArgs& p, int b) {
-  const int n = __ldg(p.lens + b);
+  const int n = p.lens[b];
   return n < 0 ? 0 : min(n, p.max_len);
 }
 
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   __shared__ int joins[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rho = lane >> 2, cl = lane & 3;
   const int units = p.c.heads * p.blocks;
+  after_previous();
 
   // ---- the line: tiles before each sequence -----------------------------------------
   // Up to 32 sequences: one per lane, in every warp alike.  More: in shared
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     const int b0 = few ? lane : tid * per, b1 = min(b0 + per, p.n_seqs);
     unsigned sum = 0;
     for (int b = b0; b < b1; ++b) {
-      const int n = __ldg(p.lens + b);
+      const int n = p.lens[b];
       if (blockIdx.x == 0 && (n < 0 || n > p.max_len)) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
       len_l = min(max(n, 0), p.max_len);
       nt_l = (len_l + TILE - 1) / TILE;
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     if (c.b != pg_seq || (unsigned)(i - pg_first) >= 32u) {
       pg_seq = c.b;
       pg_first = i;
-      pg = i + lane <= (c.len - 1) >> p.c.log_page ? __ldg(p.table + (long long)c.b * p.ld_table + i + lane) : 0;
+      pg = i + lane <= (c.len - 1) >> p.c.log_page ? p.table[(long long)c.b * p.ld_table + i + lane] : 0;
     }
     return __shfl_sync(0xFFFFFFFFu, pg, i - pg_first);
   };
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       for (int i8 = 0; i8 < DIM / 32; ++i8) {
         const int d = (i8 / (QB / 8)) * 4 * QB + QB * cl + (i8 % (QB / 8)) * 8;
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (nt * 8 + rho < gn) w = __ldg(reinterpret_cast<const uint4*>(qr + d));
+        if (nt * 8 + rho < gn) w = *reinterpret_cast<const uint4*>(qr + d);
         uint32_t* f = qf[nt] + 4 * i8;
         f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
       }
@@ -960,8 +961,7 @@ static cudaError_t launch_attn(AttnArgs& a, const AttnPlan& pl, cudaStream_t st)
   const long long all_units = (long long)a.c.heads * a.blocks * a.n_seqs;
   const long long most = need > all_units ? need : all_units;
   const int grid = (int)(most < pl.ctas ? most : pl.ctas);
-  k<<<grid, W * 32, R::BYTES, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(k, dim3(grid), W * 32, R::BYTES, st, a);
 }
 
 }  // namespace spear

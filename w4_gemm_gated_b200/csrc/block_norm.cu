@@ -45,14 +45,16 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 }
 
 // V vectors of 8 values per thread: vector j * blockDim.x + threadIdx.x of the
-// row.  All of a row's loads go out before the first sum.
+// row.  All of a row's loads go out before the first sum (the weights' too where
+// there are registers for them).
 template <int V>
 __global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant__ NormArgs p) {
   __shared__ float red[2][32];
   const long long row = blockIdx.x, base = row * p.K;
   const int nv = p.K / 8;
   const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  uint4 xw[V], yw[V], gw[V];
+  uint4 xw[V], yw[V], gw[V], post = none, pre = none;
+  after_previous();
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int i = j * blockDim.x + threadIdx.x;
@@ -60,7 +62,9 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant_
     if (i < nv) {
       if (p.y) yw[j] = *reinterpret_cast<const uint4*>(p.y + base + 8 * i);
       xw[j] = *reinterpret_cast<const uint4*>(p.x + base + 8 * i);
-      if (p.gate) gw[j] = __ldg(reinterpret_cast<const uint4*>(p.gate + row * p.gate_ld + 8 * i));
+      if (p.gate) gw[j] = *reinterpret_cast<const uint4*>(p.gate + row * p.gate_ld + 8 * i);
+      if (V == 1 && p.post) post = *reinterpret_cast<const uint4*>(p.post + 8 * i);
+      if (V == 1 && p.pre) pre = *reinterpret_cast<const uint4*>(p.pre + 8 * i);
     }
   }
   float x[V][8];
@@ -83,7 +87,8 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant_
       float u[8], w[8];
       unpack8(yw[j], u);
       if (p.post) {
-        unpack8(i < nv ? __ldg(reinterpret_cast<const uint4*>(p.post + 8 * i)) : none, w);
+        if (V > 1 && i < nv) post = *reinterpret_cast<const uint4*>(p.post + 8 * i);
+        unpack8(post, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[e] *= r * w[e];
       }
@@ -114,7 +119,8 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant_
     if (i < nv) {
       if (p.pre) {
         float w[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(p.pre + 8 * i)), w);
+        if (V > 1) pre = *reinterpret_cast<const uint4*>(p.pre + 8 * i);
+        unpack8(pre, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[j][e] *= r * w[e];
       } else {
@@ -127,9 +133,9 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant_
 }
 
 template <int V>
-static void launch_norm(const NormArgs& a, int M, cudaStream_t st) {
+static cudaError_t launch_norm(const NormArgs& a, int M, cudaStream_t st) {
   const int threads = ((a.K / 8 + V - 1) / V + 31) / 32 * 32;
-  block_norm_kernel<V><<<M, threads, 0, st>>>(a);
+  return launch_after(block_norm_kernel<V>, dim3(M), threads, 0, st, a);
 }
 
 }  // namespace spear
@@ -174,8 +180,7 @@ extern "C" int spear_block_norm(const uint16_t* x, const uint16_t* y, int M, int
   // loads to the stores counts (4096 wide: 2.4 us against 2.7 with two for one row,
   // 3.9 against 4.3 for 256); two beyond, whose loads in flight HBM needs (8192
   // rows: 53.6 us, 61.8 with one, 55.7 with four)
-  if (K <= 8192 && M <= 4 * device_sm_count()) launch_norm<1>(a, M, st);
-  else launch_norm<2>(a, M, st);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      K <= 8192 && M <= 4 * device_sm_count() ? launch_norm<1>(a, M, st) : launch_norm<2>(a, M, st);
   return e == cudaSuccess ? SPEAR_OK : set_cuda_error("block norm launch", e);
 }

@@ -146,25 +146,26 @@ __device__ __forceinline__ long long page_at(uint32_t page, uint32_t step) { ret
 
 template <int KIND, int DIM>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constant__ KvView c,
-                                                            const __nv_bfloat16* __restrict__ k, long long ld_k,
-                                                            const __nv_bfloat16* __restrict__ v, long long ld_v,
-                                                            const int* __restrict__ slots, unsigned rows,
+                                                            const __nv_bfloat16* k, long long ld_k,
+                                                            const __nv_bfloat16* v, long long ld_v,
+                                                            const int* slots, unsigned rows,
                                                             unsigned magic, WsHeader* hdr) {
   constexpr int LPR = DIM / 16, RPS = kThreads / LPR, BYTES = kv_bits(KIND);  // bytes of 8 values
   const bool is_v = blockIdx.y != 0;
   const int lane_r = threadIdx.x % LPR;
   const unsigned row0 = blockIdx.x * RPS;
   const RowIndex index(row0, c.heads);
+  after_previous();
   const int r = threadIdx.x / LPR;
   int slot = -1, head = 0;
   uint4 in[2] = {};
   if (row0 + r < rows) {
     int tok;
     index.get(r, c.heads, magic, tok, head);
-    slot = __ldg(slots + tok);
+    slot = slots[tok];
     const __nv_bfloat16* x = (is_v ? v : k) + tok * (is_v ? ld_v : ld_k) + head * DIM + lane_r * 8;
-    in[0] = __ldg(reinterpret_cast<const uint4*>(x));
-    in[1] = __ldg(reinterpret_cast<const uint4*>(x + DIM / 2));
+    in[0] = *reinterpret_cast<const uint4*>(x);
+    in[1] = *reinterpret_cast<const uint4*>(x + DIM / 2);
   }
   const int page = slot >> c.log_page;
   const bool live = slot >= 0 && page < c.n_pages;
@@ -216,14 +217,15 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
 // STEP rows per thread taken together, so that their loads are in flight together.
 template <int KIND, int DIM, int STEP>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvView c,
-                                                           const int* __restrict__ slots, unsigned rows,
-                                                           unsigned magic, __nv_bfloat16* __restrict__ k_out,
-                                                           __nv_bfloat16* __restrict__ v_out, WsHeader* hdr) {
+                                                           const int* slots, unsigned rows,
+                                                           unsigned magic, __nv_bfloat16* k_out,
+                                                           __nv_bfloat16* v_out, WsHeader* hdr) {
   constexpr int LPR = DIM / 16, RPS = kThreads / LPR, BYTES = kv_bits(KIND), WORDS = BYTES / 4;
   const bool is_v = blockIdx.y != 0;
   const int lane_r = threadIdx.x % LPR;
   const unsigned row0 = blockIdx.x * (STEP * RPS);
   const RowIndex index(row0, c.heads);
+  after_previous();
   const uint8_t* codes = (is_v ? c.v : c.k) + lane_r * BYTES;
   const __half* scales = is_v ? c.vs : c.ks;
   uint32_t in[STEP][2][WORDS];
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
     if (row0 + r < rows) {
       int tok, head;
       index.get(r, c.heads, magic, tok, head);
-      const int slot = __ldg(slots + tok);
+      const int slot = slots[tok];
       const int page = slot >> c.log_page;
       live[u] = slot >= 0 && page < c.n_pages;
       if (live[u]) {
@@ -347,12 +349,12 @@ extern "C" int spear_kv_write(const spear_kv_cache* cache, const uint16_t* k, lo
   if ((long long)n * c.heads > (1LL << 31)) return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "n=%d: too many rows", n);
   const unsigned rows = (unsigned)n * c.heads;
   const dim3 grid(blocks_for(rows, c.dim, 1), 2);
+  cudaError_t e = cudaErrorInvalidValue;
   for_kind_dim(c.kind, c.dim, [&](auto kc, auto dc) {
-    kv_write_kernel<kc.value, dc.value><<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        c, reinterpret_cast<const __nv_bfloat16*>(k), ld_k, reinterpret_cast<const __nv_bfloat16*>(v), ld_v, slots,
-        rows, magic_for(c.heads), static_cast<WsHeader*>(ws));
+    e = launch_after(kv_write_kernel<kc.value, dc.value>, grid, kThreads, 0, static_cast<cudaStream_t>(stream), c,
+                     reinterpret_cast<const __nv_bfloat16*>(k), ld_k, reinterpret_cast<const __nv_bfloat16*>(v), ld_v,
+                     slots, rows, magic_for(c.heads), static_cast<WsHeader*>(ws));
   });
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SPEAR_OK : set_cuda_error("kv write launch", e);
 }
 
@@ -371,12 +373,12 @@ extern "C" int spear_kv_read(const spear_kv_cache* cache, const int* slots, int 
   const unsigned rows = (unsigned)n * c.heads;
   const int step = step_for(rows, c.dim);
   const dim3 grid(blocks_for(rows, c.dim, step), 2);
+  cudaError_t e = cudaErrorInvalidValue;
   for_kind_dim(c.kind, c.dim, [&](auto kc, auto dc) {
     auto* f = step == 1 ? kv_read_kernel<kc.value, dc.value, 1> : kv_read_kernel<kc.value, dc.value, 2>;
-    f<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        c, slots, rows, magic_for(c.heads), reinterpret_cast<__nv_bfloat16*>(k_out),
-        reinterpret_cast<__nv_bfloat16*>(v_out), static_cast<WsHeader*>(ws));
+    e = launch_after(f, grid, kThreads, 0, static_cast<cudaStream_t>(stream), c, slots, rows, magic_for(c.heads),
+                     reinterpret_cast<__nv_bfloat16*>(k_out), reinterpret_cast<__nv_bfloat16*>(v_out),
+                     static_cast<WsHeader*>(ws));
   });
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SPEAR_OK : set_cuda_error("kv read launch", e);
 }

@@ -29,6 +29,31 @@ int check_kv_cache(const spear_kv_cache* c, KvView* out);
 
 inline bool ptr_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Start of a kernel launched by launch_after: its blocks come to the SMs while
+// the previous kernel in the stream ends (1 us saved between two of them), and
+// wait here until all that it wrote is visible.  What such a kernel reads may
+// have been written while it was on its way, so it is read by plain loads, not
+// through the read-only path (__ldg, const __restrict__).
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // f(kind, dim) as a compile-time pair.
 template <class F>
 void for_kind_dim(int kind, int dim, F f) {
