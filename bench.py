@@ -242,6 +242,8 @@ def main():
                     help="dispatch sweep (M x (K, N) x r x scale kind): time every path, check the dispatcher")
     ap.add_argument("--stack", action="store_true",
                     help="32-layer decoder stack of W4 linears (ECs on layers 0, 1, 30, 31) at M=256")
+    ap.add_argument("--decode-stack", action="store_true",
+                    help="token steps of the 32-layer stack with attention over a quantised cache")
     args = ap.parse_args()
     if args.warmup < 3:
         args.warmup = 3
@@ -261,6 +263,9 @@ def main():
         return
     if args.stack:
         run_stack(args)
+        return
+    if args.decode_stack:
+        run_decode_stack(args)
         return
 
     import torch
@@ -750,6 +755,68 @@ def stack_measure(S, synth, reps):
         "ec_bytes_fraction_of_packed_bytes": 2 * ec_params / packed_bytes,
         "output_finite": finite, "prep_seconds": round(prep_s, 1),
         "timing": f"mean of {reps} passes, weights 3.24 GB (no L2 reuse across passes)"}
+
+
+def run_decode_stack(args, n_seqs=16, context=1024):
+    """Token steps of the 32-layer stack (w4_gemm_gated_b200/decoder.py): the 224
+    linears, 32 heads of 128 over an int8 cache of `context` tokens a sequence,
+    and the norms between, eager and replayed from a CUDA graph."""
+    import torch
+
+    from w4_gemm_gated_b200 import decoder
+    from w4_gemm_gated_b200 import spear as S
+    from w4_gemm_gated_b200 import synth
+
+    reps = max(1, min(args.steps, 20))
+    dev = torch.device("cuda")
+    layers = []
+    for l in range(32):
+        row = []
+        for proj, (K, N) in enumerate(STACK_SHAPES):
+            g = torch.Generator(device=dev).manual_seed(synth.stack_layer_seed(0, l, proj))
+            row.append(S.prepare_layer(torch.randn((K, N), generator=g, device=dev) * 0.02, 0, None, None, None, 0.0))
+        layers.append(row)
+    state = decoder.make_state(layers, n_seqs, context + 256)
+    for cache in state.caches:   # earlier tokens' codes and scales
+        for t in (cache.k, cache.v):
+            t.random_(-127, 128)
+        for t in (cache.k_scales, cache.v_scales):
+            t.fill_(0.02)
+    state.seq_lens.fill_(context)
+    x = torch.randn((n_seqs, 4096), device=dev).to(torch.bfloat16)
+
+    def timed(fn):
+        ts = []
+        for _ in range(reps):
+            state.seq_lens.fill_(context)
+            decoder.advance(state)
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            fn()
+            b.record()
+            b.synchronize()
+            ts.append(a.elapsed_time(b))
+        return float(np.median(ts))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        decoder.advance(state)
+        for _ in range(2):
+            out = decoder.step(layers, x, state)
+        eager = timed(lambda: decoder.step(layers, x, state))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            decoder.step(layers, x, state)
+        graph.replay()
+        replayed = timed(graph.replay)
+    torch.cuda.synchronize()
+    assert decoder.status(state) == S.OK
+    print(json.dumps({"decode_stack": "32 layers, 224 W4 linears, 32 heads of 128, int8 cache", "n_seqs": n_seqs,
+                      "context": context, "step_ms_eager": eager, "step_ms_graph": replayed,
+                      "tokens_per_s": n_seqs / (replayed * 1e-3),
+                      "output_finite": bool(torch.isfinite(out.float()).all().item()),
+                      "timing": f"median of {reps} steps"}))
 
 
 def run_profile_case(args):
