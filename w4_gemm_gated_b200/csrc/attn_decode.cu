@@ -19,13 +19,14 @@
 // Arithmetic.  Tensor-core products over 16 tokens with the query heads as the 8
 // columns: S = K q (rows: tokens), then O^T += V^T P with P's layout turned by
 // movmatrix.  Running reference, sum and output of a softmax in fp32, in powers of
-// two; they are rescaled only when a score passes the reference.  The weight times
-// its value's scale is rounded to bf16 as the operand of the second product
-// (relative 2^-8 per weight, of the size of the output's own rounding); the sum
-// in the denominator is of the unrounded weights.  int8 codes become bf16
-// exactly, as (128 + low 7 bits) - (128 or 256 by the sign); int4 codes enter as
-// 128 + u, u = c + 8, exact, and 136 times the sum of the other operand is
-// taken off in fp32.
+// two; they are rescaled only when a weight passes the reference by 2^kSlack.
+// The operands of the second product are the weights times their values' scales:
+// as two bf16 parts for a bf16 cache; for a quantised one as fp16 (relative
+// 2^-11, under a quarter of the output's own rounding), which the reference,
+// taken of the products, keeps in its range.  The sum in the denominator is of
+// the unrounded weights.  int8 and int4 codes become fp16 as 1024 + u or 1024 + 16 u,
+// exact, and what they are too large by is taken off in fp32: by what the sums
+// start from (scores), at the end (int8) or with every product (int4).
 //
 // Joining.  A warp whose run starts or ends inside a unit leaves (maximum, sum,
 // output) in shared memory; the CTA joins the pieces of a unit in order, and
@@ -48,15 +49,20 @@ struct AttnArgs {
   long long ld_q, ld_out;
   int ld_table, max_len, n_seqs, heads, group;
   int blocks;   // units per kv head: ceil(group / (8 NT))
-  int piece;    // floats of a piece: heads of a unit x (DIM + 2)
   float scale;  // times log2(e)
   WsHeader* hdr;
-  int* tickets;  // one per CTA: arrivals at the unit that first crosses out of it
+  int ctas;      // at most
+  int* tickets;  // one per CTA: arrivals at the unit that crosses out of it first; the same of groups
   float* parts;  // two pieces per CTA
 };
 
+constexpr int kRadix = 16;    // parts of a unit joined at once; more are joined in groups of as many first
 constexpr int kMinTiles = 2;  // tiles a warp should have before more CTAs take part
-constexpr float kSlack = 8.f;  // in powers of two
+// How far, in powers of two, the largest weight may lie above 1: kept kUp above the
+// reference, up to kSlack more.  fp16 operands (to 65504) are brought to the top of
+// their range, where weights down to 2^-25 of the largest keep all their bits.
+constexpr float kUp(bool f16) { return f16 ? 11.f : 0.f; }
+constexpr float kSlack(bool f16) { return f16 ? 4.f : 8.f; }
 constexpr int kShort = 32;    // tiles up to which a unit stays in one CTA
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -99,18 +105,44 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(a), "r"(m), "r"(o));  // (a & m) | o
   return v;
 }
-// int8 codes in bytes 0 and 2 -> the two codes as bf16, exactly: two's
-// complement is the low 7 bits minus 128 times the top one.
-__device__ __forceinline__ uint32_t int8x2(uint32_t w) {
-  const uint32_t low = and_or(w, 0x007F007Fu, 0x43004300u);  // 128 + low 7 bits
-  const uint32_t top = and_or(w, 0x00800080u, 0x43004300u);  // 128 or 256
-  const __nv_bfloat162 d =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&low), *reinterpret_cast<const __nv_bfloat162*>(&top));
+__device__ __forceinline__ float log2_(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// D(16x8, fp32) += A(16x16) . B(16x8), both fp16 (F16) or both bf16.
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else mma_bf16_16816(d, a, b0, b1);
+}
+// Codes as fp16: an integer u < 1024 in the low bits of 1024 (0x6400) is 1024 + u,
+// exactly.  int8 codes, offset to u = c + 128 by kFlip, two bytes of a word at a
+// time; int4 codes u = c + 8 from bits 0-3 as 1024 + u and from bits 4-7, without
+// a shift, as 1024 + 16 u.
+constexpr uint32_t kFlip = 0x80808080u, kMagic = 0x64006400u;
+template <int SEL>
+__device__ __forceinline__ uint32_t bytes_f16(uint32_t w) {
+  return __byte_perm(w, kMagic, SEL);  // 5 and 7 pick 0x64
+}
+__device__ __forceinline__ uint32_t low4_f16(uint32_t w) { return and_or(w, 0x000F000Fu, kMagic); }
+__device__ __forceinline__ uint32_t high4_f16(uint32_t w) { return and_or(w, 0x00F000F0u, kMagic); }
+// The offsets 1024 + 8 and 1024 + 128 (of 1024 + 16 u too), to take off exactly.
+constexpr uint32_t kOff1032 = 0x64086408u, kOff1152 = 0x64806480u;
+__device__ __forceinline__ uint32_t sub2(uint32_t u, uint32_t off) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&off));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-// 4-bit codes in bits 0-3 and 16-19 -> 128 + u as bf16, exactly.
-__device__ __forceinline__ uint32_t int4x2(uint32_t w) { return and_or(w, 0x000F000Fu, 0x43004300u); }
-constexpr float kInt4Offset = 136.f;  // 128 + 8
+// The same negative, as operands.
+constexpr uint32_t kLess1152 = 0xE480E480u, kLess1032 = 0xE408E408u;
 
 // Layout of a unit's tiles in shared memory and in the fragments.
 template <int KIND, int DIM>
@@ -173,6 +205,13 @@ struct Piece {
   int b, h0, num;  // its sequence, its first query head and their number
 };
 
+// Parts of a unit to be joined: n of them from CTA `first`, `every` apart.
+struct Job {
+  int c0;  // the unit's first CTA
+  int first, every, n;
+  bool mine, group;  // this CTA joins them; they are a group, more is to come
+};
+
 // `total` tiles cut into `parts` runs of q or q + 1.
 struct Cut {
   unsigned q, more;  // the first `more` runs are one longer
@@ -220,7 +259,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   __shared__ unsigned scan_sum[W];
   __shared__ int scan_max[W];
   __shared__ Piece pieces[2 * W];  // a warp's first (unit begun before it), its last
-  __shared__ int joins[2];
+  __shared__ Job jobs[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rho = lane >> 2, cl = lane & 3;
   const int units = p.c.heads * p.blocks;
   after_previous();
@@ -237,6 +276,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     const int per = few ? 1 : (p.n_seqs + W * 32 - 1) / (W * 32);
     const int b0 = few ? lane : tid * per, b1 = min(b0 + per, p.n_seqs);
     unsigned sum = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const int n = p.lens[b];
       if (blockIdx.x == 0 && (n < 0 || n > p.max_len)) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
@@ -256,17 +296,18 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     before_l = inc - sum;
     total = __shfl_sync(ALL, inc, 31);
     if (lane < 2) pieces[2 * warp + lane].to = 0;
-    if (tid < 2) joins[tid] = 0;
     if (!few) {
       if (lane == 31) scan_sum[warp] = inc, scan_max[warp] = longest;
       __syncthreads();
       unsigned off = before_l;
       total = 0;
+#pragma unroll 1
       for (int w = 0; w < W; ++w) {
         if (w < warp) off += scan_sum[w];
         total += scan_sum[w];
         longest = max(longest, scan_max[w]);
       }
+#pragma unroll 1
       for (int b = b0; b < b1; ++b) {
         const unsigned nt = before[b];
         before[b] = off;
@@ -278,11 +319,14 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   }
   total *= units;
   // sequences without tokens
+#pragma unroll 1
   for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x)
     if (few ? __shfl_sync(ALL, nt_l, b) == 0 : before[b] == before[b + 1]) {
+#pragma unroll 1
       for (int i = tid; i < p.heads * DIM / 8; i += W * 32)
         *reinterpret_cast<uint4*>(p.out + b * p.ld_out + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
       if (p.lse)
+#pragma unroll 1
         for (int h = tid; h < p.heads; h += W * 32) p.lse[(long long)b * p.heads + h] = -INFINITY;
     }
   // ---- this CTA's and this warp's run ------------------------------------------------
@@ -366,47 +410,48 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   const uint32_t v_dst = c_row * RB + ((c_ch ^ L::xv(c_row)) << 4) + L::SIDE;
   const uint8_t* k_src = p.c.k + lane * 16;
   const uint8_t* v_src = p.c.v + lane * 16;
-  // lanes 0 to 3: 8 scales each, of K, K, V, V
-  const __half* s_src = L::QUANT ? (lane & 2 ? p.c.vs : p.c.ks) + (lane & 1) * 8 : nullptr;
-  const uint32_t s_dst = 2 * L::SIDE + (lane & 2) * TILE + (lane & 1) * 16;
-  auto copy_block = [&](uint32_t stage, int s, int t, int entry, int rows, auto whole) {
+  // even lanes: 8 scales each of K, odd ones: of V
+  const __half* s_src = L::QUANT ? (lane & 1 ? p.c.vs : p.c.ks) + (lane >> 1) * 8 : nullptr;
+  const uint32_t s_dst = 2 * L::SIDE + (lane & 1) * 2 * TILE + (lane >> 1) * 16;
+  // NB blocks of 16 tokens that lie in one page, from block s of the tile on;
+  // rows past the first `rows` of the last one (`part`), and pages that are none, are zeros.
+  auto copy_blocks = [&](uint32_t stage, int s, int t, int rows, auto nb, auto part) {
+    constexpr int NB = decltype(nb)::value;
+    const int entry = page_of(in, t);
     const bool ok = (unsigned)entry < (unsigned)p.c.n_pages;
-    const int row = (in.head << p.c.log_page) + (t & (p.c.page_size - 1));  // in the page
-    const uint32_t page = ok ? entry : 0;
-    const long long at_row = ((long long)((unsigned long long)page * p.c.page_step) << 4) + (long long)row * RB;
-    const uint32_t d = stage + 16 * s * RB;
-    // rows past the end, and pages that are none, are zeros
     if (!ok && lane == 0) report_status(p.hdr, SPEAR_ERR_DEVICE_CHECK);
-    const int live = !ok ? 0 : decltype(whole)::value ? 16 : rows;
+    const uint32_t page = ok ? entry : 0;
+    const int row = (in.head << p.c.log_page) + (t & (p.c.page_size - 1));  // in the page
+    const long long at_row = page_at(page, p.c.page_step) * 16 + row * RB;
+    const uint8_t *ks = k_src + at_row, *vs = v_src + at_row;
+    const uint32_t d = stage + 16 * s * RB;
+    const int live = ok ? rows - c_row : 0, all = ok ? 16 : 0;
 #pragma unroll
-    for (int i = 0; i < RB / 32; ++i) {
-      const int bytes = (decltype(whole)::value ? live > 0 : c_row + i * STEP < live) ? 16 : 0;
-      cp_async16(d + (k_dst ^ (L::xk(i * STEP) << 4)) + i * 512, k_src + at_row + i * 512, bytes);
-      cp_async16(d + (v_dst ^ (L::xv(i * STEP) << 4)) + i * 512, v_src + at_row + i * 512, bytes);
+    for (int i = 0; i < NB * RB / 32; ++i) {
+      const int bytes = decltype(part)::value ? (i * STEP < live ? 16 : 0) : all;
+      cp_async16(d + (k_dst ^ (L::xk(i * STEP) << 4)) + i * 512, ks + i * 512, bytes);
+      cp_async16(d + (v_dst ^ (L::xv(i * STEP) << 4)) + i * 512, vs + i * 512, bytes);
     }
     if constexpr (L::QUANT) {
-      if (lane < 4)
-        cp_async16(stage + s_dst + 32 * s, s_src + ((unsigned long long)page * p.c.scale_step << 3) + row, ok ? 16 : 0);
+      if (lane < 4 * NB)  // 8 scales each, of K and of V in turn
+        cp_async16(stage + s_dst + 32 * s, s_src + page_at(page, p.c.scale_step) * 8 + row, all);
     }
   };
   auto copy_tile = [&](uint32_t stage) {
     const int t = in.j * TILE, rows = in.len - t;
-    if (rows >= TILE) {
-      const int e0 = page_of(in, t);
-#pragma unroll
-      for (int s = 0; s < TS; ++s)
-        copy_block(stage, s, t + 16 * s, s && p.c.log_page == 4 ? page_of(in, t + 16 * s) : e0, 16, std::true_type{});
+    if (rows >= TILE && (TS == 1 || p.c.log_page > 4)) {
+      copy_blocks(stage, 0, t, 0, std::integral_constant<int, TS>{}, std::false_type{});
     } else {
-#pragma unroll
-      for (int s = 0; s < TS; ++s)
-        if (rows > 16 * s) copy_block(stage, s, t + 16 * s, page_of(in, t + 16 * s), rows - 16 * s, std::false_type{});
+#pragma unroll 1
+      for (int s = 0; s < TS && 16 * s < rows; ++s)
+        copy_blocks(stage, s, t + 16 * s, rows - 16 * s, std::integral_constant<int, 1>{}, std::true_type{});
     }
   };
 
   // ---- the run ------------------------------------------------------------------------
   float acc[MT][NT][4], m[NT][2], l[NT][2];
-  float psum[NT][4];        // int4: sums of the rounded weights
-  float kfix[NT][2];        // int4: -136 sum of q
+  float kfix[NT][2];        // quantised: what the scores' sums start from
+  float q_scale[NT][2];     // scale, and the powers of two that q was multiplied by, taken back
   uint32_t qf[NT][DIM / 8];
   int from = 0;             // first tile of the current piece
   int h0 = 0, gn = 0;       // the unit's first query head, and their number
@@ -422,8 +467,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     ++done;
     cp_commit();
   };
-  // A new piece: its query heads' values, columns past them zero ...
-  auto load_q = [&]() {
+  // A new piece: its query heads' values, columns past them zero, as B fragments
+  // in the order in which the codes' words come apart.
+  auto begin_piece = [&]() {
+    from = at.j;
     h0 = at.head * p.group + at.blk * 8 * NT;
     gn = min(8 * NT, p.group - at.blk * 8 * NT);
     constexpr int QB = KIND == SPEAR_KV_BF16 ? 8 : KIND == SPEAR_KV_INT8 ? 16 : (DIM >= 128 ? 32 : 16);
@@ -440,10 +487,6 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
       }
     }
-  };
-  // ... as B fragments, in the order in which the codes' words come apart.
-  auto begin_piece = [&]() {
-    from = at.j;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
@@ -452,29 +495,49 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       for (int a = 0; a < MT; ++a)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[a][nt][e] = 0.f;
+      q_scale[nt][0] = q_scale[nt][1] = p.scale;
+      if constexpr (L::QUANT) {
+        // to fp16, each head by the power of two that brings its largest value to
+        // 8..16, so that nothing overflows and what is lost is under 2^-28 of it
+        uint32_t m2 = 0u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) psum[nt][e] = 0.f;
-      if constexpr (KIND != SPEAR_KV_BF16) {
+        for (int k = 0; k < DIM / 8; ++k) m2 = __vmaxu2(m2, qf[nt][k] & 0x7FFF7FFFu);
+        uint32_t mag = max(m2 & 0xFFFFu, m2 >> 16);
+        mag = max(mag, __shfl_xor_sync(ALL, mag, 1));
+        mag = max(mag, __shfl_xor_sync(ALL, mag, 2));
+        const int ex = mag >> 7;  // bf16's exponent field; 0: a zero row
+        const int up = ex == 0 ? 127 : min(257 - ex, 253);
+        const float f = __uint_as_float((uint32_t)up << 23);
+        const float back = __uint_as_float((uint32_t)(254 - up) << 23);
+        q_scale[nt][0] *= __shfl_sync(ALL, back, 8 * cl);
+        q_scale[nt][1] *= __shfl_sync(ALL, back, 8 * cl + 4);
 #pragma unroll
         for (int i8 = 0; i8 < DIM / 32; ++i8) {
-          uint32_t* f = qf[nt] + 4 * i8;
-          const uint4 w = make_uint4(f[0], f[1], f[2], f[3]);
-          if constexpr (KIND == SPEAR_KV_INT8) {  // bytes 0, 2 and 1, 3 of a word
-            f[0] = __byte_perm(w.x, w.y, 0x5410), f[1] = __byte_perm(w.x, w.y, 0x7632);
-            f[2] = __byte_perm(w.z, w.w, 0x5410), f[3] = __byte_perm(w.z, w.w, 0x7632);
-          } else {  // nibbles i and i + 4 of a word
-            f[0] = __byte_perm(w.x, w.z, 0x5410), f[1] = __byte_perm(w.x, w.z, 0x7632);
-            f[2] = __byte_perm(w.y, w.w, 0x5410), f[3] = __byte_perm(w.y, w.w, 0x7632);
+          uint32_t* w = qf[nt] + 4 * i8;
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[2 * k] = __uint_as_float(w[k] << 16) * f;
+            x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * f;
+          }
+          if constexpr (KIND == SPEAR_KV_INT8) {  // bytes 0, 1 and 2, 3 of a word
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = pack_f16x2(x[2 * k], x[2 * k + 1]);
+          } else {  // nibbles i and i + 4 of a word, the odd ones in sixteenths
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float part = k & 1 ? 0.0625f : 1.f;
+              w[k] = pack_f16x2(x[k] * part, x[k + 4] * part);
+            }
           }
         }
-      }
-      if constexpr (KIND == SPEAR_KV_INT4) {
-        const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        const uint32_t even = KIND == SPEAR_KV_INT8 ? kLess1152 : kLess1032;
+        const uint32_t less[4] = {even, even, kLess1152, kLess1152};
         float sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < DIM / 8; k += 2) mma_bf16_16816(sq, ones, qf[nt][k], qf[nt][k + 1]);
-        kfix[nt][0] = -kInt4Offset * sq[0];
-        kfix[nt][1] = -kInt4Offset * sq[1];
+        for (int k = 0; k < DIM / 8; k += 2) mma<true>(sq, less, qf[nt][k], qf[nt][k + 1]);
+        kfix[nt][0] = sq[0];
+        kfix[nt][1] = sq[1];
       }
     }
   };
@@ -483,7 +546,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   auto work = [&](const uint32_t st, const int rows, auto whole) {
     constexpr bool WHOLE = decltype(whole)::value;
     // ---- scores: S[token][head] --------------------------------------------------------
-    float s[TS][NT][4];
+    float s[TS][NT][4], sv[TS][2];  // scores; the values' scales of this lane's two tokens
     float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
@@ -493,7 +556,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[b][nt][e] = KIND == SPEAR_KV_INT4 ? kfix[nt][e & 1] : 0.f;
+          for (int e = 0; e < 4; ++e) s[b][nt][e] = L::QUANT ? kfix[nt][e & 1] : 0.f;
         const uint32_t ka = st + (16 * b + r0) * RB, kb = st + (16 * b + r1) * RB;
 #pragma unroll
         for (int i4 = 0; i4 < L::KI; ++i4) {
@@ -510,42 +573,45 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
             for (int k = 0; k < 4; k += 2) {
               const uint32_t a[4] = {x[k], y[k], x[k + 1], y[k + 1]};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[b][nt], a, qf[nt][4 * i4 + k], qf[nt][4 * i4 + k + 1]);
+              for (int nt = 0; nt < NT; ++nt) mma<false>(s[b][nt], a, qf[nt][4 * i4 + k], qf[nt][4 * i4 + k + 1]);
             }
           } else if constexpr (KIND == SPEAR_KV_INT8) {
 #pragma unroll
             for (int k = 0; k < L::KW; ++k) {
-              const uint32_t a[4] = {int8x2(x[k]), int8x2(y[k]), int8x2(x[k] >> 8), int8x2(y[k] >> 8)};
+              x[k] ^= kFlip, y[k] ^= kFlip;
+              const uint32_t a[4] = {bytes_f16<0x5150>(x[k]), bytes_f16<0x5150>(y[k]), bytes_f16<0x5352>(x[k]),
+                                     bytes_f16<0x5352>(y[k])};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_bf16_16816(s[b][nt], a, qf[nt][2 * (L::KW * i4 + k)], qf[nt][2 * (L::KW * i4 + k) + 1]);
+                mma<true>(s[b][nt], a, qf[nt][2 * (L::KW * i4 + k)], qf[nt][2 * (L::KW * i4 + k) + 1]);
             }
           } else {
 #pragma unroll
             for (int k = 0; k < L::KW; ++k)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t a[4] = {int4x2(x[k] >> (8 * h)), int4x2(y[k] >> (8 * h)), int4x2(x[k] >> (8 * h + 4)),
-                                       int4x2(y[k] >> (8 * h + 4))};
+                const uint32_t xh = h ? x[k] >> 8 : x[k], yh = h ? y[k] >> 8 : y[k];
+                const uint32_t a[4] = {low4_f16(xh), low4_f16(yh), high4_f16(xh), high4_f16(yh)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                  mma_bf16_16816(s[b][nt], a, qf[nt][4 * (L::KW * i4 + k) + 2 * h],
-                                 qf[nt][4 * (L::KW * i4 + k) + 2 * h + 1]);
+                  mma<true>(s[b][nt], a, qf[nt][4 * (L::KW * i4 + k) + 2 * h], qf[nt][4 * (L::KW * i4 + k) + 2 * h + 1]);
               }
           }
         }
-        float f0 = p.scale, f1 = p.scale;
+        float f0 = 1.f, f1 = 1.f;
         if constexpr (L::QUANT) {
           const uint32_t sa = st + 2 * L::SIDE + 32 * b;
-          f0 *= lds_half(sa + 2 * r0);
-          f1 *= lds_half(sa + 2 * r1);
+          f0 = lds_half(sa + 2 * r0);
+          f1 = lds_half(sa + 2 * r1);
+          sv[b][0] = lds_half(sa + 2 * TILE + 2 * r0);
+          sv[b][1] = lds_half(sa + 2 * TILE + 2 * r1);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[b][nt][e] *= f0;
-            s[b][nt][e + 2] *= f1;
+            s[b][nt][e] *= f0 * q_scale[nt][e];
+            s[b][nt][e + 2] *= f1 * q_scale[nt][e];
           }
         if (!WHOLE) {
 #pragma unroll
@@ -556,21 +622,24 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
               if (16 * b + r1 >= rows) s[b][nt][e + 2] = -INFINITY;
             }
         }
+        // of the weight times its value's scale (at least fp16's smallest)
+        const float g0 = L::QUANT ? fmaxf(log2_(sv[b][0]), -24.f) : 0.f;
+        const float g1 = L::QUANT ? fmaxf(log2_(sv[b][1]), -24.f) : 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[b][nt][e], s[b][nt][e + 2]));
+          for (int e = 0; e < 2; ++e)
+            top[nt][e] = fmaxf(top[nt][e], fmaxf(s[b][nt][e] + g0, s[b][nt][e + 2] + g1));
       }
     }
     // ---- the weights' reference m; what is there is scaled down where it moves -------------
-    // m follows the maximum only once a score lies more than kSlack above it: a
-    // weight of up to 2^kSlack does no harm in fp32 and bf16, and most tiles need
-    // neither the maximum over lanes nor new factors.
+    // m follows the maximum only once a weight is kSlack too large, which does no
+    // harm: most tiles need neither the maximum over lanes nor new factors.
     bool above = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) above |= top[nt][e] > m[nt][e] + kSlack;
+      for (int e = 0; e < 2; ++e) above |= top[nt][e] > m[nt][e] + (kUp(L::QUANT) + kSlack(L::QUANT));
     if (__any_sync(ALL, above)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -579,7 +648,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(ALL, top[nt][e], d));
-          const float now = fmaxf(top[nt][e], m[nt][e]);
+          const float now = fmaxf(top[nt][e] - kUp(L::QUANT), m[nt][e]);
           f[e] = m[nt][e] == -INFINITY ? 0.f : exp2_(m[nt][e] - now);
           m[nt][e] = now;
           l[nt][e] *= f[e];
@@ -588,8 +657,6 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         for (int a = 0; a < MT; ++a)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[a][nt][e] *= f[e & 1];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) psum[nt][e] *= f[e & 1];
       }
     }
     float ref[NT][2];  // scores of -infinity alone leave m there: their weights are 0
@@ -603,15 +670,13 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       if (WHOLE || 16 * b < rows) {
         float f0 = 1.f, f1 = 1.f;
         if constexpr (L::QUANT) {
-          const uint32_t sa = st + 2 * L::SIDE + 2 * TILE + 32 * b;
-          f0 = lds_half(sa + 2 * r0);
-          f1 = lds_half(sa + 2 * r1);
+          f0 = sv[b][0], f1 = sv[b][1];
           if (!WHOLE) {  // scales of rows past the end may be anything
             if (16 * b + r0 >= rows) f0 = 0.f;
             if (16 * b + r1 >= rows) f1 = 0.f;
           }
         }
-        uint32_t pb[NT][2];
+        uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float e[4];
@@ -619,11 +684,16 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
           for (int k = 0; k < 4; ++k) e[k] = exp2_(s[b][nt][k] - ref[nt][k & 1]);
           l[nt][0] += e[0] + e[2];
           l[nt][1] += e[1] + e[3];
-          pb[nt][0] = movmatrix(pack_bf16x2(e[0] * f0, e[1] * f0));
-          pb[nt][1] = movmatrix(pack_bf16x2(e[2] * f1, e[3] * f1));
-          if constexpr (KIND == SPEAR_KV_INT4) {
-            const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-            mma_bf16_16816(psum[nt], ones, pb[nt][0], pb[nt][1]);
+          if constexpr (L::QUANT) {
+            pb[nt][0] = movmatrix(pack_f16x2(e[0] * f0, e[1] * f0));
+            pb[nt][1] = movmatrix(pack_f16x2(e[2] * f1, e[3] * f1));
+          } else {
+            // two bf16 parts; HBM leaves the time for the second product
+            const uint32_t h0 = pack_bf16x2(e[0], e[1]), h1 = pack_bf16x2(e[2], e[3]);
+            pb[nt][0] = movmatrix(h0);
+            pb[nt][1] = movmatrix(h1);
+            pl[nt][0] = movmatrix(pack_bf16x2(e[0] - __uint_as_float(h0 << 16), e[1] - __uint_as_float(h0 & 0xFFFF0000u)));
+            pl[nt][1] = movmatrix(pack_bf16x2(e[2] - __uint_as_float(h1 << 16), e[3] - __uint_as_float(h1 & 0xFFFF0000u)));
           }
         }
         const uint32_t va = st + L::SIDE + 16 * b * RB;
@@ -651,26 +721,32 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
             if constexpr (KIND == SPEAR_KV_BF16) {
               const uint32_t a[4] = {lo01, hi01, lo89, hi89};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                mma<false>(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
+                mma<false>(acc[a0][nt], a, pl[nt][0], pl[nt][1]);
+              }
             } else if constexpr (KIND == SPEAR_KV_INT8) {
-              const uint32_t a[4] = {int8x2(lo01), int8x2(lo01 >> 8), int8x2(lo89), int8x2(lo89 >> 8)};
-              const uint32_t c[4] = {int8x2(hi01), int8x2(hi01 >> 8), int8x2(hi89), int8x2(hi89 >> 8)};
+              const uint32_t l01 = lo01 ^ kFlip, h01 = hi01 ^ kFlip, l89 = lo89 ^ kFlip, h89 = hi89 ^ kFlip;
+              const uint32_t a[4] = {sub2(bytes_f16<0x5250>(l01), kOff1152), sub2(bytes_f16<0x5351>(l01), kOff1152), sub2(bytes_f16<0x5250>(l89), kOff1152),
+                                     sub2(bytes_f16<0x5351>(l89), kOff1152)};
+              const uint32_t c[4] = {sub2(bytes_f16<0x5250>(h01), kOff1152), sub2(bytes_f16<0x5351>(h01), kOff1152), sub2(bytes_f16<0x5250>(h89), kOff1152),
+                                     sub2(bytes_f16<0x5351>(h89), kOff1152)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma_bf16_16816(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
-                mma_bf16_16816(acc[a0 + 1][nt], c, pb[nt][0], pb[nt][1]);
+                mma<true>(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
+                mma<true>(acc[a0 + 1][nt], c, pb[nt][0], pb[nt][1]);
               }
             } else {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t a[4] = {int4x2(lo01 >> (8 * h)), int4x2(lo01 >> (8 * h + 4)), int4x2(lo89 >> (8 * h)),
-                                       int4x2(lo89 >> (8 * h + 4))};
-                const uint32_t c[4] = {int4x2(hi01 >> (8 * h)), int4x2(hi01 >> (8 * h + 4)), int4x2(hi89 >> (8 * h)),
-                                       int4x2(hi89 >> (8 * h + 4))};
+                const uint32_t l01 = h ? lo01 >> 8 : lo01, l89 = h ? lo89 >> 8 : lo89;
+                const uint32_t h01 = h ? hi01 >> 8 : hi01, h89 = h ? hi89 >> 8 : hi89;
+                const uint32_t a[4] = {sub2(low4_f16(l01), kOff1032), sub2(high4_f16(l01), kOff1152), sub2(low4_f16(l89), kOff1032), sub2(high4_f16(l89), kOff1152)};
+                const uint32_t c[4] = {sub2(low4_f16(h01), kOff1032), sub2(high4_f16(h01), kOff1152), sub2(low4_f16(h89), kOff1032), sub2(high4_f16(h89), kOff1152)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  mma_bf16_16816(acc[a0 + h][nt], a, pb[nt][0], pb[nt][1]);
-                  mma_bf16_16816(acc[a0 + 2 + h][nt], c, pb[nt][0], pb[nt][1]);
+                  mma<true>(acc[a0 + h][nt], a, pb[nt][0], pb[nt][1]);
+                  mma<true>(acc[a0 + 2 + h][nt], c, pb[nt][0], pb[nt][1]);
                 }
               }
             }
@@ -680,11 +756,11 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     }
   };
 
-  if (n > 0) load_q();
 #pragma unroll 1
   for (int i = 0; i < R::STAGES - 1; ++i) issue();
-  if (n > 0) begin_piece();
+  bool fresh = true;
   for (int i = 0; i < n; ++i) {
+    if (fresh) begin_piece();
     cp_wait<R::STAGES - 2>();
     __syncwarp();  // tile i is in, and every lane is through with tile i - 1
     issue();
@@ -692,72 +768,66 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     if (rows >= TILE) work(take, rows, std::true_type{});
     else work(take, rows, std::false_type{});
     take = take + L::STAGE == ring_end ? ring_a : take + L::STAGE;
-    // ---- the end of the unit or of the run -----------------------------------------------------
-    const bool unit_ends = at.j + 1 == at.nt;
-    if (unit_ends || i + 1 == n) {
+    // ---- the end of the unit or of the run ------------------------------------------------
+    // What runs once or twice a launch is kept short rather than fast, here and
+    // below: lines of code that the stream through L2 has pushed out take long to come.
+    fresh = at.j + 1 == at.nt;
+    if (fresh || i + 1 == n) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], d);
-      if constexpr (KIND == SPEAR_KV_INT4) {
+          for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(ALL, l[nt][e], d);
+      if (fresh && from == 0) {  // the whole unit: out with it
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int a = 0; a < MT; ++a)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[a][nt][e] = fmaf(-kInt4Offset, psum[nt][e & 1], acc[a][nt][e]);
-      }
-      const bool whole = unit_ends && from == 0;
-      if (!unit_ends) {
-        // every copy is in and read: the ring is this piece's place
-        cp_wait<0>();
-        __syncwarp();
-      }
-      float* dst = unit_ends ? first_piece : last_piece;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int h = nt * 8 + 2 * cl + e;
-          if (h < gn) {
-            if (whole) {
-              const float inv = 1.f / l[nt][e];
+          for (int e = 0; e < 2; ++e) {
+            const int h = nt * 8 + 2 * cl + e;
+            if (h < gn) {
+              const float even = 1.f / l[nt][e], odd = KIND == SPEAR_KV_INT4 ? 0.0625f * even : even;
               __nv_bfloat16* o = p.out + at.b * p.ld_out + (long long)(h0 + h) * DIM;
 #pragma unroll
               for (int a = 0; a < MT; a += 4) {
                 const int d = (a / (L::VL / 2)) * 8 * L::VL + rho * L::VL + 2 * (a % (L::VL / 2));
                 uint4 w;
-                w.x = pack_bf16x2(acc[a][nt][e] * inv, acc[a][nt][e + 2] * inv);
-                w.y = pack_bf16x2(acc[a + 1][nt][e] * inv, acc[a + 1][nt][e + 2] * inv);
-                w.z = pack_bf16x2(acc[a + 2][nt][e] * inv, acc[a + 2][nt][e + 2] * inv);
-                w.w = pack_bf16x2(acc[a + 3][nt][e] * inv, acc[a + 3][nt][e + 2] * inv);
+                w.x = pack_bf16x2(acc[a][nt][e] * even, acc[a][nt][e + 2] * odd);
+                w.y = pack_bf16x2(acc[a + 1][nt][e] * even, acc[a + 1][nt][e + 2] * odd);
+                w.z = pack_bf16x2(acc[a + 2][nt][e] * even, acc[a + 2][nt][e + 2] * odd);
+                w.w = pack_bf16x2(acc[a + 3][nt][e] * even, acc[a + 3][nt][e + 2] * odd);
                 *reinterpret_cast<uint4*>(o + d) = w;
               }
               if (p.lse && rho == 0)
                 p.lse[(long long)at.b * p.heads + h0 + h] = (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
-            } else {
-#pragma unroll
-              for (int a = 0; a < MT; ++a) {
-                const int d = (a / (L::VL / 2)) * 8 * L::VL + rho * L::VL + 2 * (a % (L::VL / 2));
-                *reinterpret_cast<float2*>(dst + h * DIM + d) = make_float2(acc[a][nt][e], acc[a][nt][e + 2]);
-              }
-              if (rho == 0) {
-                dst[gn * DIM + h] = m[nt][e];
-                dst[gn * DIM + gn + h] = l[nt][e];
-              }
             }
           }
+      } else {
+        if (!fresh) {
+          // every copy is in and read: the ring is this piece's place
+          cp_wait<0>();
+          __syncwarp();
         }
-      if (!whole && lane == 0)
-        pieces[2 * warp + (unit_ends ? 0 : 1)] = {t0 + i - at.j, at.nt, from, at.j + 1, at.b, h0, gn};
+        float* dst = fresh ? first_piece : last_piece;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int h = nt * 8 + 2 * cl + e;
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+              const int d = (a / (L::VL / 2)) * 8 * L::VL + rho * L::VL + 2 * (a % (L::VL / 2));
+              *reinterpret_cast<float2*>(dst + h * DIM + d) = make_float2(acc[a][nt][e], acc[a][nt][e + 2]);
+            }
+            if (rho == 0) {
+              dst[8 * NT * DIM + h] = m[nt][e];
+              dst[8 * NT * DIM + 8 * NT + h] = l[nt][e];
+            }
+          }
+        if (lane == 0) pieces[2 * warp + !fresh] = {t0 + i - at.j, at.nt, from, at.j + 1, at.b, h0, gn};
+      }
     }
     advance<TILE>(p, at);
-    if (unit_ends && i + 1 < n) {
-      load_q();
-      begin_piece();
-    }
   }
   cp_wait<0>();
   __syncthreads();
@@ -774,11 +844,12 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     if (part) {
       __stcg(reinterpret_cast<float4*>(part + h * DIM + d), o);
       if (d == 0) {
-        __stcg(part + pc.num * DIM + h, mx);
-        __stcg(part + pc.num * DIM + pc.num + h, sum);
+        __stcg(part + 8 * NT * DIM + h, mx);
+        __stcg(part + 8 * NT * DIM + 8 * NT + h, sum);
       }
     } else {
       const float inv = 1.f / sum;
+      if constexpr (KIND == SPEAR_KV_INT4) o.y *= 0.0625f, o.w *= 0.0625f;  // odd dims, from bits 4-7
       *reinterpret_cast<uint2*>(p.out + pc.b * p.ld_out + (long long)(pc.h0 + h) * DIM + d) =
           make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
       if (p.lse && d == 0) p.lse[(long long)pc.b * p.heads + pc.h0 + h] = (mx + log2f(sum)) * 0.6931471805599453f;
@@ -795,9 +866,9 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     float pm = -INFINITY, w = 0.f, sum = 0.f;
     const bool has = set >> lane & 1;
     if (has) {
-      const float* f = piece_of(lane) + pc.num * DIM + h;
+      const float* f = piece_of(lane) + 8 * NT * DIM + h;
       pm = f[0];
-      sum = f[pc.num];
+      sum = f[8 * NT];
     }
     float mx = pm;
 #pragma unroll
@@ -809,7 +880,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     for (int e = 8; e > 0; e >>= 1) sum += __shfl_xor_sync(ALL, sum, e);
     sum = __shfl_sync(ALL, sum, 0);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 1
     for (; set; set &= set - 1) {
       const int k = __ffs(set) - 1;
       const float wk = __shfl_sync(ALL, w, k);
@@ -822,48 +893,61 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     }
     put_item(pc, item, mx, sum, o, part);
   };
-  // Parts of `count` CTAs from c0 on, read past this SM's L1, eight in flight.
-  auto join_parts = [&](const Piece& pc, int item, int first, int count) {
-    const int h = item / CH, d = (item % CH) * 128 + 4 * lane;
-    if (h >= pc.num) return;
-    constexpr int STEP = 8;
-    float mx = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // Where CTA c of a unit that begins in CTA c0 has its part: the first on its far side.
+  auto part_of = [&](int c, int c0) { return p.parts + ((size_t)c * 2 + (c == c0)) * R::PIECE; };
+  // The parts of `count` CTAs, `every` apart from `first` on, read past this SM's L1, to
+  // the output or to `part`: each warp has up to I items, of STEP parts at a time, all
+  // asked for before any is used.
+  auto join_parts = [&](const Piece& pc, int c0, int first, int every, int count, float* part) {
+    constexpr int I = (8 * NT * CH + W - 1) / W, STEP = 16 / I;
+    float mx[I], sum[I];
+    float4 o[I];
+#pragma unroll
+    for (int c = 0; c < I; ++c) mx[c] = -INFINITY, sum[c] = 0.f, o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int k0 = 0; k0 < count; k0 += STEP) {
-      float pm[STEP], pl[STEP];
-      float4 pv[STEP];
+      float pm[I][STEP], pl[I][STEP];
+      float4 pv[I][STEP];
 #pragma unroll
       for (int k = 0; k < STEP; ++k) {
-        pm[k] = -INFINITY;
-        pl[k] = 0.f;
-        pv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + k < count) {
-          // the unit's first CTA has it on its far side
-          const float* f = p.parts + ((size_t)(first + k0 + k) * 2 + (k0 + k == 0)) * p.piece;
-          pm[k] = __ldcg(f + pc.num * DIM + h);
-          pl[k] = __ldcg(f + pc.num * DIM + pc.num + h);
-          if (4 * lane < LD) pv[k] = __ldcg(reinterpret_cast<const float4*>(f + h * DIM + d));
+        const float* f = part_of(first + (k0 + k) * every, c0);
+#pragma unroll
+        for (int c = 0; c < I; ++c) {
+          const int item = warp + c * W, h = item / CH, d = (item % CH) * 128 + 4 * lane;
+          pm[c][k] = -INFINITY;
+          pl[c][k] = 0.f;
+          pv[c][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k0 + k < count && h < pc.num) {
+            pm[c][k] = __ldcg(f + 8 * NT * DIM + h);
+            pl[c][k] = __ldcg(f + 8 * NT * DIM + 8 * NT + h);
+            if (4 * lane < LD) pv[c][k] = __ldcg(reinterpret_cast<const float4*>(f + h * DIM + d));
+          }
         }
       }
-      float top = mx;
 #pragma unroll
-      for (int k = 0; k < STEP; ++k) top = fmaxf(top, pm[k]);
-      const float keep = mx == -INFINITY ? 0.f : exp2_(mx - top);
-      mx = top;
-      sum *= keep;
-      o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+      for (int c = 0; c < I; ++c) {
+        float top = mx[c];
 #pragma unroll
-      for (int k = 0; k < STEP; ++k) {
-        const float w = k0 + k < count ? exp2_(pm[k] - mx) : 0.f;
-        sum = fmaf(w, pl[k], sum);
-        o.x = fmaf(w, pv[k].x, o.x);
-        o.y = fmaf(w, pv[k].y, o.y);
-        o.z = fmaf(w, pv[k].z, o.z);
-        o.w = fmaf(w, pv[k].w, o.w);
+        for (int k = 0; k < STEP; ++k) top = fmaxf(top, pm[c][k]);
+        const float keep = mx[c] == -INFINITY ? 0.f : exp2_(mx[c] - top);
+        mx[c] = top;
+        sum[c] *= keep;
+        o[c].x *= keep, o[c].y *= keep, o[c].z *= keep, o[c].w *= keep;
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) {
+          const float w = k0 + k < count ? exp2_(pm[c][k] - top) : 0.f;
+          sum[c] = fmaf(w, pl[c][k], sum[c]);
+          o[c].x = fmaf(w, pv[c][k].x, o[c].x);
+          o[c].y = fmaf(w, pv[c][k].y, o[c].y);
+          o[c].z = fmaf(w, pv[c][k].z, o[c].z);
+          o[c].w = fmaf(w, pv[c][k].w, o[c].w);
+        }
       }
     }
-    put_item(pc, item, mx, sum, o, nullptr);
+    if (part) __syncthreads();  // it may be one of those just read
+#pragma unroll
+    for (int c = 0; c < I; ++c)
+      if ((warp + c * W) / CH < pc.num) put_item(pc, warp + c * W, mx[c], sum[c], o[c], part);
   };
   // Lane i of every warp looks at piece i; a unit's pieces are neighbours among those
   // that are there.  heads: the first piece of each unit.
@@ -882,35 +966,66 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     float* part = nullptr;
     if (!(starts && ends)) {
       open[starts] = k;
-      part = p.parts + ((size_t)blockIdx.x * 2 + starts) * p.piece;
+      part = p.parts + ((size_t)blockIdx.x * 2 + starts) * R::PIECE;
     }
     // the items of all units are dealt to the warps in turn
     for (; at_item < items; at_item += W) join_here(pieces[k], at_item, set, part);
     at_item -= items;
   }
   if (open[0] < 0 && open[1] < 0) return;
-  // The parts of every thread are ordered before the count by the barrier and its
-  // release, and read after its acquire by whoever counts last.
-  int c0[2], c1[2];  // the CTAs that the open units span
-  for (int side = 0; side < 2; ++side)
-    if (open[side] >= 0) {
-      const Piece& pc = pieces[open[side]];
-      c0[side] = cut.owner(pc.start);
-      c1[side] = cut.owner(pc.start + pc.nt - 1);
-    }
-  __syncthreads();
+  // Who counts last at a unit's ticket, which is then back at zero, joins its parts;
+  // of many, first those of its group, to the place of the group's first.  Thread 0
+  // sees to the one unit, thread 1 to the other.  Every thread's parts are ordered
+  // before the count by the barrier and its release, and those of others are read
+  // after its acquire.
+  Job job = {};
+  int* ticket = nullptr;
+  int count = 0;
   if (tid < 2 && open[tid] >= 0) {
-    int* ticket = p.tickets + c0[tid];
-    int old;
-    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
-    joins[tid] = old == c1[tid] - c0[tid];
-    if (joins[tid]) *ticket = 0;
+    const Piece& pc = pieces[open[tid]];
+    job.c0 = job.first = cut.owner(pc.start);
+    job.every = 1;
+    job.n = count = cut.owner(pc.start + pc.nt - 1) - job.c0 + 1;
+    ticket = p.tickets + job.c0;
+    if (count > kRadix) {
+      job.group = true;
+      job.first += (int)(blockIdx.x - job.c0) / kRadix * kRadix;
+      job.n = min(kRadix, job.c0 + count - job.first);
+      ticket = p.tickets + p.ctas + job.first;
+    }
   }
-  __syncthreads();
-  for (int side = 0; side < 2; ++side)
-    if (joins[side])
-      for (int item = warp; item < items; item += W)
-        join_parts(pieces[open[side]], item, c0[side], c1[side] - c0[side] + 1);
+#pragma unroll 1
+  for (bool more = true; more;) {
+    __syncthreads();
+    if (tid < 2) {
+      job.mine = false;
+      if (ticket) {
+        int old;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
+        job.mine = old == job.n - 1;
+        if (job.mine) *ticket = 0;
+      }
+      jobs[tid] = job;
+      if (!job.mine || !job.group) {
+        ticket = nullptr;
+      } else {  // then the groups' parts
+        job.group = false;
+        job.first = job.c0;
+        job.every = kRadix;
+        job.n = (count + kRadix - 1) / kRadix;
+        ticket = p.tickets + job.c0;
+      }
+    }
+    __syncthreads();
+    more = false;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const Job j = jobs[side];
+      if (!j.mine) continue;
+      join_parts(pieces[open[side]], j.c0, j.first, j.every, j.n, j.group ? part_of(j.first, j.c0) : nullptr);
+      more |= j.group;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -926,8 +1041,7 @@ static AttnPlan plan_attn(const KvView& c, int n_q_heads) {
   const int group = n_q_heads / c.heads;
   a.nt = group > 8 && c.dim < 256 ? 2 : 1;
   a.blocks = (group + 8 * a.nt - 1) / (8 * a.nt);
-  const int in_unit = group < 8 * a.nt ? group : 8 * a.nt;
-  a.piece = (in_unit * (c.dim + 2) + 3) / 4 * 4;
+  a.piece = (8 * a.nt * (c.dim + 2) + 3) / 4 * 4;  // Room::PIECE
   a.ctas = device_sm_count() * attn_per_sm(c.kind, c.dim);
   return a;
 }
@@ -935,7 +1049,7 @@ static AttnPlan plan_attn(const KvView& c, int n_q_heads) {
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 static size_t attn_ws_bytes(const AttnPlan& a) {
-  return kWsHeaderBytes + up256(a.ctas * sizeof(int)) + up256((size_t)a.ctas * 2 * a.piece * sizeof(float));
+  return kWsHeaderBytes + up256(2 * a.ctas * sizeof(int)) + up256((size_t)a.ctas * 2 * a.piece * sizeof(float));
 }
 
 template <int KIND, int DIM, int NT>
@@ -1022,12 +1136,12 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   a.heads = n_q_heads;
   a.group = n_q_heads / a.c.heads;
   a.blocks = pl.blocks;
-  a.piece = pl.piece;
   a.scale = scale * 1.4426950408889634f;
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.hdr = reinterpret_cast<WsHeader*>(w);
   a.tickets = reinterpret_cast<int*>(w + kWsHeaderBytes);
-  a.parts = reinterpret_cast<float*>(w + kWsHeaderBytes + up256(pl.ctas * sizeof(int)));
+  a.parts = reinterpret_cast<float*>(w + kWsHeaderBytes + up256(2 * pl.ctas * sizeof(int)));
+  a.ctas = pl.ctas;
   cudaError_t e = cudaErrorInvalidValue;
   for_kind_dim(a.c.kind, a.c.dim, [&](auto kc, auto dc) {
     if constexpr (dc.value < 256)

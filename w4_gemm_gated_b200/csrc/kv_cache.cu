@@ -142,7 +142,6 @@ __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[WOR
   }
 }
 
-__device__ __forceinline__ long long page_at(uint32_t page, uint32_t step) { return (long long)((uint64_t)page * step); }
 
 template <int KIND, int DIM>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constant__ KvView c,

@@ -29,6 +29,9 @@ int check_kv_cache(const spear_kv_cache* c, KvView* out);
 
 inline bool ptr_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Distance to a page, in 16-byte steps.
+__device__ __forceinline__ long long page_at(uint32_t page, uint32_t step) { return (long long)((uint64_t)page * step); }
+
 // Start of a kernel launched by launch_after: its blocks come to the SMs while
 // the previous kernel in the stream ends (1 us saved between two of them), and
 // wait here until all that it wrote is visible.  What such a kernel reads may
