@@ -6,8 +6,8 @@
 // that share it (two operations per value and head).
 //
 // Work.  A unit is one (sequence, kv head) with up to 8 NT query heads; its
-// tokens are cut into tiles of TILE.  All units' tiles in order form one line,
-// which is cut into equal runs, one per CTA and in it one per warp, by the
+// tokens are cut into tiles of TILE.  All units' tiles in order form one line
+// (with a step for each unit besides), which is cut into equal runs, one per CTA and in it one per warp, by the
 // lengths alone (every CTA sums them up): ragged batches load the machine
 // evenly, a long sequence is spread over many warps, and a warp takes many
 // short ones without meeting anybody.  Where every unit is short the CTAs'
@@ -176,8 +176,7 @@ __device__ __forceinline__ int clamp_len(const AttnArgs& p, int b) {
   return n < 0 ? 0 : min(n, p.max_len);
 }
 
-// A place on the line of tiles: sequence, kv head, block of its query heads,
-// tile of the unit.
+// A place on the line: sequence, kv head, block of its query heads, tile of the unit.
 struct Place {
   int b, head, blk, j, nt, len;
 };
@@ -199,7 +198,7 @@ __device__ __forceinline__ void advance(const AttnArgs& p, Place& c) {
 
 // A warp's unfinished part of a unit.
 struct Piece {
-  unsigned start;  // the unit's first tile on the line, which names the unit
+  unsigned start;  // the unit's begin on the line, which names the unit
   int nt;          // its tiles
   int from, to;    // tiles [from, to); to = 0: no piece
   int b, h0, num;  // its sequence, its first query head and their number
@@ -212,7 +211,7 @@ struct Job {
   bool mine, group;  // this CTA joins them; they are a group, more is to come
 };
 
-// `total` tiles cut into `parts` runs of q or q + 1.
+// A line of `total` cut into `parts` runs of q or q + 1.
 struct Cut {
   unsigned q, more;  // the first `more` runs are one longer
   __device__ __forceinline__ Cut(unsigned total, unsigned parts) : q(total / parts), more(total - q * parts) {}
@@ -252,11 +251,11 @@ template <int KIND, int DIM, int NT, int W, int PER_SM>
 __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_constant__ AttnArgs p) {
   using L = Lay<KIND, DIM>;
   using R = Room<KIND, DIM, NT>;
-  static_assert(R::BYTES >= 4 * (kMaxSeqs + 1), "the line lies in the rings' place");
+  static_assert(R::BYTES >= 8 * (kMaxSeqs + 1), "the line lies in the rings' place");
   constexpr int TILE = L::TILE, TS = L::TS, RB = L::RB, MT = DIM / 16;
   constexpr unsigned ALL = 0xFFFFFFFFu;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ unsigned scan_sum[W];
+  __shared__ unsigned scan_sum[W], scan_live[W];
   __shared__ int scan_max[W];
   __shared__ Piece pieces[2 * W];  // a warp's first (unit begun before it), its last
   __shared__ Job jobs[2];
@@ -264,18 +263,22 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   const int units = p.c.heads * p.blocks;
   after_previous();
 
-  // ---- the line: tiles before each sequence -----------------------------------------
+  // ---- the line -----------------------------------------------------------------------
+  // Every unit takes as many steps of it as it has tiles and one before them, since
+  // to begin and to end a unit costs about what a tile does (a warp that got the 28
+  // units of a one-token sequence for its 28 tiles took half as long again).
   // Up to 32 sequences: one per lane, in every warp alike.  More: in shared
   // memory, in the rings' place, a run of `per` to each thread.
   const bool few = p.n_seqs <= 32;
-  unsigned* before = reinterpret_cast<unsigned*>(smem);  // n_seqs + 1 of them
+  unsigned* before = reinterpret_cast<unsigned*>(smem);  // steps of one unit of each sequence before it, n_seqs + 1
+  unsigned* seqs = before + p.n_seqs + 1;                // sequences before it that have tokens
   int len_l = 0, nt_l = 0;                               // few: this lane's sequence
-  unsigned before_l = 0, total;
+  unsigned before_l = 0, total, all_live = 0;
   int longest = 0;                                       // tiles of the longest unit
   {
     const int per = few ? 1 : (p.n_seqs + W * 32 - 1) / (W * 32);
     const int b0 = few ? lane : tid * per, b1 = min(b0 + per, p.n_seqs);
-    unsigned sum = 0;
+    unsigned sum = 0, live = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const int n = p.lens[b];
@@ -283,40 +286,49 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       len_l = min(max(n, 0), p.max_len);
       nt_l = (len_l + TILE - 1) / TILE;
       if (!few) before[b] = nt_l;
-      sum += nt_l;
+      sum += nt_l + (nt_l > 0);
+      live += nt_l > 0;
       longest = max(longest, nt_l);
     }
-    unsigned inc = sum;
+    auto scan = [&](unsigned v) {  // of the lanes before this one and this one
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const unsigned o = __shfl_up_sync(ALL, inc, d);
-      if (lane >= d) inc += o;
-    }
+      for (int d = 1; d < 32; d <<= 1) {
+        const unsigned o = __shfl_up_sync(ALL, v, d);
+        if (lane >= d) v += o;
+      }
+      return v;
+    };
+    const unsigned inc = scan(sum);
     longest = __reduce_max_sync(ALL, longest);
     before_l = inc - sum;
     total = __shfl_sync(ALL, inc, 31);
     if (lane < 2) pieces[2 * warp + lane].to = 0;
     if (!few) {
-      if (lane == 31) scan_sum[warp] = inc, scan_max[warp] = longest;
+      const unsigned inc_live = scan(live);
+      if (lane == 31) scan_sum[warp] = inc, scan_live[warp] = inc_live, scan_max[warp] = longest;
       __syncthreads();
-      unsigned off = before_l;
+      unsigned off = before_l, off_live = inc_live - live;
       total = 0;
 #pragma unroll 1
       for (int w = 0; w < W; ++w) {
-        if (w < warp) off += scan_sum[w];
+        if (w < warp) off += scan_sum[w], off_live += scan_live[w];
         total += scan_sum[w];
+        all_live += scan_live[w];
         longest = max(longest, scan_max[w]);
       }
 #pragma unroll 1
       for (int b = b0; b < b1; ++b) {
         const unsigned nt = before[b];
         before[b] = off;
-        off += nt;
+        seqs[b] = off_live;
+        off += nt + (nt > 0);
+        off_live += nt > 0;
       }
       if (tid == 0) before[p.n_seqs] = total;
       __syncthreads();
     }
   }
+  const unsigned seq_units = units * (few ? __popc(__ballot_sync(ALL, nt_l > 0)) : all_live);
   total *= units;
   // sequences without tokens
 #pragma unroll 1
@@ -338,28 +350,36 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   const unsigned ctas = min(gridDim.x, aligned ? min(total, (unsigned)(p.n_seqs * units))
                                                : (total + kMinTiles * W - 1) / (kMinTiles * W));
   if (blockIdx.x >= ctas) return;  // nothing for this CTA
-  auto place = [&](unsigned t) {   // of tile t < total, the same in every lane
+  // Step t < total: the tile that comes at it or next; r: steps into its unit;
+  // starts: units that start before t.
+  auto place = [&](unsigned t, unsigned& r, unsigned& starts) {
     Place c;
-    unsigned first;  // the sequence's first tile
+    unsigned first;  // the sequence's first step
     if (few) {
+      const unsigned live = __ballot_sync(ALL, nt_l > 0);
       c.b = 31 - __clz(__ballot_sync(ALL, nt_l > 0 && before_l * units <= t));
       first = __shfl_sync(ALL, before_l, c.b) * units;
       c.nt = __shfl_sync(ALL, nt_l, c.b);
       c.len = __shfl_sync(ALL, len_l, c.b);
+      starts = __popc(live & ((1u << c.b) - 1u)) * units;
     } else {
       // the last b with before[b] * units <= t, 32 candidates at a time
       int b = 0;
+#pragma unroll 1
       for (int step = p.n_seqs > 1024 ? 1024 : 32; step > 0; step >>= 5) {
         const int i = b + lane * step;
         b += step * (31 - __clz(__ballot_sync(ALL, i < p.n_seqs && before[i] * units <= t)));
       }
       c.b = b;
       first = before[b] * units;
-      c.nt = before[b + 1] - before[b];
+      c.nt = before[b + 1] - before[b] - 1;
       c.len = clamp_len(p, b);
+      starts = seqs[b] * units;
     }
-    const unsigned r = t - first, u = r / c.nt;
-    c.j = r - u * c.nt;
+    const unsigned u = (t - first) / (c.nt + 1);
+    r = t - first - u * (c.nt + 1);
+    starts += u + (r > 0);
+    c.j = r ? r - 1 : 0;
     c.head = u;
     c.blk = 0;
     if (p.blocks > 1) {
@@ -370,20 +390,34 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   };
   const Cut cut(total, ctas);
   unsigned c_begin = cut.begin(blockIdx.x), c_end = cut.begin(blockIdx.x + 1);
-  if (aligned) {
-    auto up = [&](unsigned t) {  // the next unit's start from t on
-      if (t >= total) return total;
-      const Place c = place(t);
-      return c.j ? t + c.nt - c.j : t;
-    };
-    c_begin = up(c_begin);
-    c_end = up(c_end);
+  unsigned start = 0;  // the begin of the unit that is worked on
+  int n = 0;           // tiles
+  Place in = {};       // next tile to copy
+#pragma unroll 1
+  for (int k = aligned ? 0 : 2; k < 4; ++k) {  // the CTA's begin and end, this warp's begin, and its end
+    const Cut mine(c_end - c_begin, W);
+    const unsigned t = k == 0 ? c_begin : k == 1 ? c_end : c_begin + mine.begin(k == 2 ? warp : warp + 1);
+    unsigned r = 0, starts = seq_units;
+    Place c = {};
+    if (t < total) c = place(t, r, starts);
+    const unsigned up = r ? t + c.nt + 1 - r : t;  // the next unit's start
+    if (k == 0) {
+      c_begin = up;
+    } else if (k == 1) {
+      c_end = up;
+    } else if (k == 2) {
+      in = c;
+      start = t - r;
+      n = c_begin + mine.begin(warp + 1) - t;  // steps
+      if (t + n <= start + c.nt + 1) {         // in one unit
+        n -= r == 0 && n > 0;
+        break;
+      }
+      n = starts - t;  // tiles before the run, to be taken from those before its end
+    } else {
+      n += t - starts;
+    }
   }
-  const Cut mine(c_end - c_begin, W);
-  const unsigned t0 = c_begin + mine.begin(warp);
-  const int n = mine.begin(warp + 1) - mine.begin(warp);
-  Place in = {};  // next tile to copy
-  if (n > 0) in = place(t0);
   Place at = in;  // tile to work on
   if (!few) __syncthreads();  // the rings take over `before`'s place
 
@@ -824,9 +858,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
               dst[8 * NT * DIM + 8 * NT + h] = l[nt][e];
             }
           }
-        if (lane == 0) pieces[2 * warp + !fresh] = {t0 + i - at.j, at.nt, from, at.j + 1, at.b, h0, gn};
+        if (lane == 0) pieces[2 * warp + !fresh] = {start, at.nt, from, at.j + 1, at.b, h0, gn};
       }
     }
+    if (fresh) start += at.nt + 1;
     advance<TILE>(p, at);
   }
   cp_wait<0>();
@@ -983,9 +1018,9 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   int count = 0;
   if (tid < 2 && open[tid] >= 0) {
     const Piece& pc = pieces[open[tid]];
-    job.c0 = job.first = cut.owner(pc.start);
+    job.c0 = job.first = cut.owner(pc.start + 1);
     job.every = 1;
-    job.n = count = cut.owner(pc.start + pc.nt - 1) - job.c0 + 1;
+    job.n = count = cut.owner(pc.start + pc.nt) - job.c0 + 1;
     ticket = p.tickets + job.c0;
     if (count > kRadix) {
       job.group = true;
@@ -1069,8 +1104,8 @@ static cudaError_t launch_attn(AttnArgs& a, const AttnPlan& pl, cudaStream_t st)
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   // no more CTAs than the longest possible line gives work to
-  const long long tiles = (long long)a.c.heads * a.blocks * a.n_seqs * ((a.max_len + L::TILE - 1) / L::TILE);
-  if (tiles >> 31) return cudaErrorInvalidConfiguration;  // refused before
+  const long long tiles = (long long)a.c.heads * a.blocks * a.n_seqs * ((a.max_len + L::TILE - 1) / L::TILE + 1);
+  if (tiles >> 32) return cudaErrorInvalidConfiguration;  // refused before
   const long long need = (tiles + (long long)kMinTiles * W - 1) / ((long long)kMinTiles * W);
   const long long all_units = (long long)a.c.heads * a.blocks * a.n_seqs;
   const long long most = need > all_units ? need : all_units;
