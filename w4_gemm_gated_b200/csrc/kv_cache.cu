@@ -58,22 +58,19 @@ __device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t w) { return __v
 // Rows of the calls: token-major, DIM / 16 lanes per row, each with the two
 // chunks of 8 values that lie DIM / 2 apart (so that every load and store of a
 // warp is of whole sectors).  At large sizes both calls are as near the issue
-// rate as HBM, so what a row costs beside its values is spread over 16 of them:
-// with 8 per lane 47,000 tokens of 8 int8 heads took 40.5 us to read back (now
-// 33.0, the bytes alone 27.8) and 8,000 18.0 us to write (now 11.5, 6.8).
+// rate as HBM, so what a row costs beside its values is spread over 16 of them (8
+// per lane: 40.5 us to read back where it is 33.0, 18.0 to write where it is 11.5).
+// 29,300 tokens of 8 int8 heads are read back in 31.7 us, 87 % of what a copy of as
+// many bytes reaches, 7,200 written in 11.2 us, 60 % (of bf16 heads 96 and 84 %).
 constexpr int kThreads = 256;
 
-// Token and head of row `row0 + r` of a block, from the first row's.
-struct RowIndex {
-  int tok0, head0;
-  __device__ __forceinline__ RowIndex(unsigned row0, int heads) : tok0(row0 / heads), head0(row0 % heads) {}
-  __device__ __forceinline__ void get(int r, int heads, unsigned magic, int& tok, int& head) const {
-    const unsigned x = head0 + r;  // under 2^12, where the product's high half is the quotient
-    const unsigned t = heads == 1 ? x : __umulhi(x, magic);
-    tok = tok0 + t;
-    head = x - t * heads;
-  }
-};
+// Token and head of a row.  magic = floor(2^32 / heads): the product's high half is
+// the quotient or one less.
+__device__ __forceinline__ void split_row(unsigned row, unsigned heads, unsigned magic, unsigned& tok, unsigned& head) {
+  tok = heads == 1 ? row : __umulhi(row, magic);
+  head = row - tok * heads;
+  if (head >= heads) ++tok, head -= heads;
+}
 
 // Two fp32 values in one register pair, and operations on both.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -98,11 +95,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // 8 bf16 values -> codes c = clamp(rint(x / s), -Q, Q) of the IEEE quotient, as bytes.
 //
 // x has 8 significant bits and s 11, so a quotient of at most 128 that is no tie
-// (k + 1/2) is at least 1 / (2 * 2047) = 2.4e-4 away from one; x * (1 / s) is
-// within 2^-22 * 128 = 3.1e-5 of it.  Rounded to a multiple of 2^-13 (by adding
-// 1.5 * 2^10, where that is the spacing; off by 6.1e-5 more at most), a tie
-// becomes the tie exactly and nothing else does, and rounding that to an
-// integer (by adding 1.5 * 2^23, whose low byte then holds it) is the definition's.
+// (k + 1/2) is at least 1 / (2 * 2047) = 2.4e-4 away from one; x * (1 / s), with a
+// reciprocal of up to 2 ulp, is within 2^-21.6 * 128 = 4e-5 of it.  Rounded to a
+// multiple of 2^-13 (by adding 1.5 * 2^10, where that is the spacing; off by 6.1e-5
+// more at most), a tie becomes the tie exactly and nothing else does, and rounding
+// that to an integer (by adding 1.5 * 2^23, whose low byte then holds it) is the
+// definition's.
 // clamp: the row's scale was cut or is below fp16's normal range, so that
 // quotients pass Q (elsewhere they stay under Q (1 + 2^-11), which rounds to Q).
 template <int Q>
@@ -142,7 +140,6 @@ __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[WOR
   }
 }
 
-
 template <int KIND, int DIM>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constant__ KvView c,
                                                             const __nv_bfloat16* k, long long ld_k,
@@ -152,15 +149,13 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
   constexpr int LPR = DIM / 16, RPS = kThreads / LPR, BYTES = kv_bits(KIND);  // bytes of 8 values
   const bool is_v = blockIdx.y != 0;
   const int lane_r = threadIdx.x % LPR;
-  const unsigned row0 = blockIdx.x * RPS;
-  const RowIndex index(row0, c.heads);
+  const unsigned row = blockIdx.x * RPS + threadIdx.x / LPR;
+  unsigned tok, head;
+  split_row(row, c.heads, magic, tok, head);
   after_previous();
-  const int r = threadIdx.x / LPR;
-  int slot = -1, head = 0;
+  int slot = -1;
   uint4 in[2] = {};
-  if (row0 + r < rows) {
-    int tok;
-    index.get(r, c.heads, magic, tok, head);
+  if (row < rows) {
     slot = slots[tok];
     const __nv_bfloat16* x = (is_v ? v : k) + tok * (is_v ? ld_v : ld_k) + head * DIM + lane_r * 8;
     in[0] = *reinterpret_cast<const uint4*>(x);
@@ -192,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
     const bool zero = sf == 0.f || sf != sf;  // codes 0: nothing there, or a NaN that the scale keeps
     if (sf == 0.f) hs = __float2half_rn(1.f);
     if (zero) sf = 1.f;
-    const float inv = 1.f / sf;
+    const float inv = __fdividef(1.f, sf);
     const bool clamp = __any_sync(0xFFFFFFFFu, sf < 6.103515625e-5f || sf >= 65504.f || zero);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -223,7 +218,6 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
   const bool is_v = blockIdx.y != 0;
   const int lane_r = threadIdx.x % LPR;
   const unsigned row0 = blockIdx.x * (STEP * RPS);
-  const RowIndex index(row0, c.heads);
   after_previous();
   const uint8_t* codes = (is_v ? c.v : c.k) + lane_r * BYTES;
   const __half* scales = is_v ? c.vs : c.ks;
@@ -235,8 +229,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
     const int r = u * RPS + threadIdx.x / LPR;
     live[u] = false;
     if (row0 + r < rows) {
-      int tok, head;
-      index.get(r, c.heads, magic, tok, head);
+      unsigned tok, head;
+      split_row(row0 + r, c.heads, magic, tok, head);
       const int slot = slots[tok];
       const int page = slot >> c.log_page;
       live[u] = slot >= 0 && page < c.n_pages;
@@ -309,11 +303,11 @@ static int blocks_for(long long rows, int dim, int step) {
 }
 
 // Rows per thread when reading back: one while the blocks are few, where only a
-// call's latency counts (440 tokens: 2.2 us, 2.5 with two), two beyond (47,000
-// tokens: 33.0 us, 35.2 with one, 36.5 with four).
+// call's latency counts (330 tokens of 8 int8 heads: 1.85 us, 2.3 with two), two
+// beyond (29,300: 31.7 us, 33.4 with one; four were 10 % slower than two).
 static int step_for(long long rows, int dim) { return blocks_for(rows, dim, 1) <= 4 * device_sm_count() ? 1 : 2; }
 
-static unsigned magic_for(int heads) { return heads == 1 ? 0u : 0xFFFFFFFFu / heads + 1; }
+static unsigned magic_for(int heads) { return (unsigned)((1ull << 32) / heads); }
 
 }  // namespace spear
 
