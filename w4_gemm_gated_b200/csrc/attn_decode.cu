@@ -2,15 +2,20 @@
 //
 //   out_h = sum_t p_t v_t,  p = softmax(scale q_h . k_t)
 //
-// Bound by HBM: each cached byte is read once and used for the few query heads
-// that share it (two operations per value and head).
+// Each cached byte is read once and used for the few query heads that share it (two
+// operations per value and head), so HBM bounds it in principle, and does for
+// bf16: 2 sequences of up to 131,072 tokens, 8 heads of 128, 800 MB in 128 us, 6.2
+// TB/s.  Quantised caches take a few instructions per code, which bound them where
+// no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 68 us, 4.0 TB/s at 58 %
+// of the issue rate).  Short batches are bound by the chain from the lengths over
+// the page table to the data and by the joins (int8, 16 x 2048: 36 MB in 17 us).
 //
 // Work.  A unit is one (sequence, kv head) with up to 8 NT query heads; its
 // tokens are cut into tiles of TILE.  All units' tiles in order form one line
-// (with a step for each unit besides), which is cut into equal runs, one per CTA and in it one per warp, by the
-// lengths alone (every CTA sums them up): ragged batches load the machine
-// evenly, a long sequence is spread over many warps, and a warp takes many
-// short ones without meeting anybody.  Where every unit is short the CTAs'
+// (with a step for each unit besides), which is cut into equal runs, one per CTA
+// and in it one per warp, by the lengths alone (every CTA sums them up): ragged
+// batches load the machine evenly, a long sequence is spread over many warps, and
+// a warp takes many short ones without meeting anybody.  Where every unit is short the CTAs'
 // borders move to units' borders (see Cut).  A warp streams its run through its own ring of shared-memory
 // stages (16-byte asynchronous copies, rows past a sequence's end filled with
 // zeros), so that copies cross the units' borders and never wait for another
@@ -225,7 +230,8 @@ struct Cut {
 // Warps of a CTA and CTAs of an SM.  Two CTAs, so that one streams while the other
 // starts or joins (bf16, 64 x 4096: one of 8 warps 108 us, two of 4 101, four of 2
 // 103).  Quantised kinds are bound by their arithmetic and take 16 warps where 128
-// registers do (two of 8; four of 4 cost more joins: 16 x 2048 int8 16.9 us, 18.6).
+// registers do (two of 8; with two of 4 int8 of 16 x 2048 takes 18.1 us, not 17.0, and
+// int4 of 32 x 4099 with 32 heads 73.0, not 68.4).
 constexpr bool attn_small(int kind, int dim, int nt) { return kind != SPEAR_KV_BF16 && dim < 256 && nt == 1; }
 constexpr int attn_warps(int kind, int dim, int nt) { return attn_small(kind, dim, nt) ? 8 : 4; }
 constexpr int attn_per_sm(int kind, int dim) { return kind == SPEAR_KV_BF16 && dim == 256 ? 1 : 2; }
@@ -345,7 +351,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   // Where no unit is longer than kShort tiles, CTAs take whole units: the borders
   // of even runs move on to the next unit's start.  A CTA may then have up to
   // kShort tiles more than its share, which costs no more than joining a unit
-  // across CTAs does (97 tokens, 8 units: 7.4 us, 15.5 with joins), and saves that.
+  // across CTAs does and saves that (7 sequences to 1001 tokens, 2 heads of 64: 9.0 us,
+  // 10.7 with joins; a single sequence of 97, 8 heads, pays for it: 5.9 us, 5.4).
   const bool aligned = longest <= kShort;
   const unsigned ctas = min(gridDim.x, aligned ? min(total, (unsigned)(p.n_seqs * units))
                                                : (total + kMinTiles * W - 1) / (kMinTiles * W));

@@ -3,8 +3,9 @@
 //     x_out = a x + b gate u,   h = x_out * rsqrt(mean(x_out^2) + eps) * pre
 // in fp32, each output rounded once to bf16.  One CTA per row; the row stays in
 // registers between the two reductions, so x and y are read once and x_out
-// and h written once: bound by HBM at many rows, by the launch and the two
-// block reductions at few.
+// and h written once: bound by HBM at many rows (8192 x 4096 with a gate per token:
+// 336 MB in 53 us, 6.3 TB/s), by the launch and the two block reductions at few
+// (one row of 4096: 2.0 us).
 #include "kv_cache.cuh"
 
 namespace spear {
@@ -176,11 +177,12 @@ extern "C" int spear_block_norm(const uint16_t* x, const uint16_t* y, int M, int
                       reinterpret_cast<__nv_bfloat16*>(x_out), reinterpret_cast<__nv_bfloat16*>(h), gate_ld, K,
                       residual_scale, block_scale, eps};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // one vector per thread while a row has an SM to itself, where the chain from the
-  // loads to the stores counts (4096 wide: 2.4 us against 2.7 with two for one row,
-  // 3.9 against 4.3 for 256); two beyond, whose loads in flight HBM needs (8192
-  // rows: 53.6 us, 61.8 with one, 55.7 with four)
-  const cudaError_t e =
-      K <= 8192 && M <= 4 * device_sm_count() ? launch_norm<1>(a, M, st) : launch_norm<2>(a, M, st);
+  // One vector per thread while the machine takes all of the call's threads at 1024
+  // per SM, where the chain from the loads to the stores counts (4096 wide, one row:
+  // 2.0 us against 2.3 with two; 256 rows: 2.9, 3.3); two beyond, whose loads in
+  // flight HBM needs (8192 wide, 256 rows: 3.6 us, 5.6 with one; 5120 wide, 8192
+  // rows: 51.7, 74.5, with four 52.6)
+  const bool one_each = K <= 8192 && (long long)M * K <= 8192LL * device_sm_count();
+  const cudaError_t e = one_each ? launch_norm<1>(a, M, st) : launch_norm<2>(a, M, st);
   return e == cudaSuccess ? SPEAR_OK : set_cuda_error("block norm launch", e);
 }
