@@ -67,6 +67,16 @@ def test_splits(S, kind, lens, heads):
     _run(S, f, 2, seed=4)
 
 
+@pytest.mark.parametrize("kind,seqs,tokens", [("int8", 18, 6400), ("bf16", 9, 9600), ("int4", 18, 12800)])
+def test_long_units_that_meet_in_a_cta(S, kind, seqs, tokens):
+    # units over 17 or 33 CTAs, whose last is the next one's first: each joins its
+    # parts in groups of 16, the last group of the one and the first of the other there
+    f = Filled(S, kind, [tokens] * seqs, 1, 64 if kind == "bf16" else 128, 64, seed=seqs)
+    _, out, lse, ws = _run(S, f, 4, seed=6)
+    _, again, lse2, _ = _run(S, f, 4, seed=6, ws=ws)  # the counters are back at zero
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_more_sequences_than_threads(S):
     lens = [(i * 7) % 23 for i in range(1500)]
     f = Filled(S, "int8", lens, 1, 64, 16, seed=3)

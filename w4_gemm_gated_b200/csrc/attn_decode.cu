@@ -57,7 +57,7 @@ struct AttnArgs {
   float scale;  // times log2(e)
   WsHeader* hdr;
   int ctas;      // at most
-  int* tickets;  // one per CTA: arrivals at the unit that crosses out of it first; the same of groups
+  int* tickets;  // one per CTA: arrivals at the unit that crosses out of it first; two per CTA: at its parts' groups
   float* parts;  // two pieces per CTA
 };
 
@@ -1033,7 +1033,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       job.group = true;
       job.first += (int)(blockIdx.x - job.c0) / kRadix * kRadix;
       job.n = min(kRadix, job.c0 + count - job.first);
-      ticket = p.tickets + p.ctas + job.first;
+      // a unit's last CTA may be the first of another's: each counts on its part's side
+      ticket = p.tickets + p.ctas + 2 * job.first + (job.first == job.c0);
     }
   }
 #pragma unroll 1
@@ -1091,7 +1092,7 @@ static AttnPlan plan_attn(const KvView& c, int n_q_heads) {
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 static size_t attn_ws_bytes(const AttnPlan& a) {
-  return kWsHeaderBytes + up256(2 * a.ctas * sizeof(int)) + up256((size_t)a.ctas * 2 * a.piece * sizeof(float));
+  return kWsHeaderBytes + up256(3 * a.ctas * sizeof(int)) + up256((size_t)a.ctas * 2 * a.piece * sizeof(float));
 }
 
 template <int KIND, int DIM, int NT>
@@ -1182,7 +1183,7 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.hdr = reinterpret_cast<WsHeader*>(w);
   a.tickets = reinterpret_cast<int*>(w + kWsHeaderBytes);
-  a.parts = reinterpret_cast<float*>(w + kWsHeaderBytes + up256(2 * pl.ctas * sizeof(int)));
+  a.parts = reinterpret_cast<float*>(w + kWsHeaderBytes + up256(3 * pl.ctas * sizeof(int)));
   a.ctas = pl.ctas;
   cudaError_t e = cudaErrorInvalidValue;
   for_kind_dim(a.c.kind, a.c.dim, [&](auto kc, auto dc) {
