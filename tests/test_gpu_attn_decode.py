@@ -145,6 +145,30 @@ def test_nan_in_a_live_row_stays_in_its_head(S):
     assert np.all(np.isfinite(out))
 
 
+@pytest.mark.parametrize("hidden", [40, 1000, 9000, 9999])
+def test_scores_of_minus_infinity_have_no_weight(S, hidden):
+    # the first `hidden` keys are -infinity in a dim where q is positive: whole tiles,
+    # warps' runs and CTAs' parts of no weight; a second sequence has nothing else
+    f = Filled(S, "bf16", [10000, 70], 2, 64, 16, seed=hidden)
+    pages = f.table.long().cpu()
+    for b, n in ((0, hidden), (1, 70)):
+        t = torch.arange(n)
+        f.cache.k[pages[b, t // 16].cuda(), :, (t % 16).cuda(), 5] = float("-inf")
+        f.k[b][:n, :, 5] = -np.inf
+    q = _q(2, 4, 64, 8)
+    q[:, :, 5] = 1.5
+    ws = S.make_attn_workspace(f.cache, 4)
+    lse = torch.zeros(2, 4, device="cuda")
+    out = S.attn_decode(q, f.cache, f.table, f.seq_lens, ws, lse=lse)
+    assert S.read_status(ws) == S.OK
+    assert torch.isnan(out[1]).all() and torch.equal(lse[1], torch.full_like(lse[1], float("-inf")))
+    # the sequence as if it began behind them
+    g = Filled.__new__(Filled)
+    g.kind, g.lens, g.heads, g.dim = f.kind, [10000 - hidden], f.heads, f.dim
+    g.k, g.v = [f.k[0][hidden:]], [f.v[0][hidden:]]
+    g.check(S, q[:1], out[:1], lse[:1], 64 ** -0.5, ws)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "int4"])
 def test_bad_pages_are_reported_and_skipped(S, kind):
     f = Filled(S, kind, [40, 40, 40], 2, 64, 16, seed=14)

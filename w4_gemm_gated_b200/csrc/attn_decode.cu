@@ -877,6 +877,9 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   // ---- join the pieces of each unit -----------------------------------------------------------
   constexpr int CH = (DIM + 127) / 128;      // 128-value parts of a head: one per warp and step
   constexpr int LD = DIM >= 128 ? 128 : DIM;  // values of such a part
+  // Of a piece of maximum pm where mx is the largest so far; its sums are
+  // 0 where all its scores are -infinity, and 0 / 0 follows where all pieces' are.
+  auto weight = [&](float pm, float mx) { return pm == -INFINITY ? 0.f : exp2_(pm - mx); };
   // Part `item` (head, part) of a unit's pieces joined: their common maximum
   // mx and sum, and LD values o of the output, one float4 per lane.  It goes to the
   // output, or to `part` where pieces of other CTAs are still to come.
@@ -916,7 +919,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
     for (int e = 8; e > 0; e >>= 1) mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, e));  // 2 W <= 16 pieces
     mx = __shfl_sync(ALL, mx, 0);
-    if (has) w = exp2_(pm - mx);
+    if (has) w = weight(pm, mx);
     sum *= w;
 #pragma unroll
     for (int e = 8; e > 0; e >>= 1) sum += __shfl_xor_sync(ALL, sum, e);
@@ -977,7 +980,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         o[c].x *= keep, o[c].y *= keep, o[c].z *= keep, o[c].w *= keep;
 #pragma unroll
         for (int k = 0; k < STEP; ++k) {
-          const float w = k0 + k < count ? exp2_(pm[c][k] - top) : 0.f;
+          const float w = k0 + k < count ? weight(pm[c][k], top) : 0.f;
           sum[c] = fmaf(w, pl[c][k], sum[c]);
           o[c].x = fmaf(w, pv[c][k].x, o[c].x);
           o[c].y = fmaf(w, pv[c][k].y, o[c].y);
