@@ -276,8 +276,8 @@ size_t spear_kv_page_scales(int kind, int page_size, int n_heads, int head_dim);
 int spear_kv_write(const spear_kv_cache* cache, const uint16_t* k, long long ld_k, const uint16_t* v, long long ld_v,
                    const int* slots, int n, void* ws, size_t ws_bytes, void* stream);
 
-/* Read n tokens back: k_out, v_out device bf16 [n][n_heads][head_dim] (dense),
- * bf16_rne(c * s).  Slots may repeat; a negative slot's rows are zeros, and so
+/* Read n tokens back: k_out, v_out device bf16 [n][n_heads][head_dim] (dense, apart
+ * from one another), bf16_rne(c * s).  Slots may repeat; a negative slot's rows are zeros, and so
  * are those of a slot past the cache's end, which is reported as above. */
 int spear_kv_read(const spear_kv_cache* cache, const int* slots, int n, uint16_t* k_out, uint16_t* v_out, void* ws,
                   size_t ws_bytes, void* stream);
@@ -289,8 +289,8 @@ int spear_kv_read(const spear_kv_cache* cache, const int* slots, int n, uint16_t
  *     lse = log(sum_t exp(s_t)).
  * A sequence without tokens has out = 0 and lse = -inf.
  * q, out     device bf16, n_seqs rows of n_q_heads * head_dim; ld_q, ld_out:
- *            elements between rows (multiples of 8, at least a row).  They must
- *            not overlap.
+ *            elements between rows (multiples of 8, at least a row).  They may
+ *            be column ranges of the same rows; any other overlap is refused.
  * n_q_heads  a multiple of the cache's n_heads, at most 1024.
  * page_table device int32, n_seqs rows of max_pages entries, ld_table apart:
  *            token t of sequence b lies in page page_table[b][t / page_size].

@@ -192,6 +192,31 @@ def test_block_norm_refusals(S, kw, code):
 
 
 # ---- refusals of the binding ----------------------------------------------------------
+@pytest.mark.parametrize("out,ld,seqs", [
+    (0x1000, 4096, 1), (0x1010, 4096, 2), (0x2FF0, 4096, 1), (0x1000 + 4096, 6144, 2), (0x1000 + 8192, 4104, 2),
+    (0x1000 + 8192 - 16, 16384, 3), (0x1000 + 2 * 16384 - 8192 + 16, 16384, 3),
+])
+def test_attn_refuses_overlaps_of_q_and_out(S, out, ld, seqs):
+    rc = S.F["spear_attn_decode"](ctypes.byref(_cache(S)), 0x1000, ld, seqs, 32, 0x900000, 4, 4, 0xA00000, 0.1, out, ld,
+                                  None, 0x600000, 255, None)
+    assert rc == 1 and "overlap" in S.F["spear_last_error"]().decode()
+
+
+@pytest.mark.parametrize("out,ld,seqs", [
+    (0x1000 + 8192, 4096, 1), (0x1000 + 8192, 8192, 5), (0x1000 + 2 * 16384 - 8192, 16384, 3),
+    (0x1000 + 32768 + 8192, 16384, 3), (0x100000 - 8192, 4096, 1),
+])
+def test_attn_takes_q_and_out_as_columns_of_the_same_rows(S, out, ld, seqs):
+    # past the check, the workspace is refused
+    assert S.F["spear_attn_decode"](ctypes.byref(_cache(S)), 0x1000, ld, seqs, 32, 0x900000, 4, 4, 0xA00000, 0.1, out, ld,
+                                    None, 0x600000, 255, None) == 4
+
+
+@pytest.mark.parametrize("v", [0x1000, 0x1010, 0x1000 + 4 * 1024 * 2 - 16, 0x1000 - 16])
+def test_kv_read_refuses_overlapping_outputs(S, v):
+    assert S.F["spear_kv_read"](ctypes.byref(_cache(S)), 0x300000, 4, 0x1000, v, 0x400000, 256, None) == 1
+
+
 def test_binding_refuses_host_tensors_and_wrong_types(S):
     z = torch.zeros
     with pytest.raises(TypeError):

@@ -1150,7 +1150,6 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   if (n_seqs == 0) return SPEAR_OK;
   if (!q || !page_table || !seq_lens || !out || !ws) return set_error(SPEAR_ERR_INVALID_ARG, "NULL pointer");
   if (!(fabsf(scale) < INFINITY)) return set_error(SPEAR_ERR_INVALID_ARG, "scale=%g: must be finite", scale);
-  if (q == out) return set_error(SPEAR_ERR_INVALID_ARG, "q and out are the same buffer");
   if (max_pages < 1 || ld_table < max_pages)
     return set_error(SPEAR_ERR_INVALID_ARG, "max_pages=%d ld_table=%d: 1 <= max_pages <= ld_table", max_pages, ld_table);
   if ((long long)max_pages * a.c.page_size > 0x7fff0000LL)
@@ -1166,6 +1165,13 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   for (const void* p : {(const void*)page_table, (const void*)seq_lens, (const void*)lse})
     if (reinterpret_cast<uintptr_t>(p) & 3u)
       return set_error(SPEAR_ERR_ALIGNMENT, "page_table, seq_lens and lse must be 4-byte aligned");
+  // q and out may be column ranges of the same rows, and share nothing else
+  if (buffers_meet(q, ((n_seqs - 1) * ld_q + row) * 2, out, ((n_seqs - 1) * ld_out + row) * 2)) {
+    const long long apart = (long long)(reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(q)) / 2;
+    const long long column = (apart % ld_q + ld_q) % ld_q;
+    if (n_seqs == 1 || ld_q != ld_out || column < row || column + row > ld_q)
+      return set_error(SPEAR_ERR_INVALID_ARG, "q and out overlap");
+  }
   const AttnPlan pl = plan_attn(a.c, n_q_heads);
   const size_t need = attn_ws_bytes(pl);
   if (ws_bytes < need) return set_error(SPEAR_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);

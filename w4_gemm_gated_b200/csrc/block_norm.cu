@@ -163,15 +163,12 @@ extern "C" int spear_block_norm(const uint16_t* x, const uint16_t* y, int M, int
     if (!ptr_aligned16(p)) return set_error(SPEAR_ERR_ALIGNMENT, "unaligned pointer");
   // outputs may be x or y, element for element, and overlap nothing else
   const uintptr_t rows = (uintptr_t)M * K * 2, one = (uintptr_t)K * 2;
-  auto meet = [](const void* p, uintptr_t np, const void* q, uintptr_t nq) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return p && q && a < b + nq && b < a + np;
-  };
   for (const uint16_t* o : {(const uint16_t*)x_out, (const uint16_t*)h})
-    if ((o != x && meet(o, rows, x, rows)) || (o != y && meet(o, rows, y, rows)) || meet(o, rows, post_weight, one) ||
-        meet(o, rows, pre_weight, one) || meet(o, rows, gate, (uintptr_t)(M - 1) * gate_ld * 2 + one))
+    if ((o != x && buffers_meet(o, rows, x, rows)) || (o != y && buffers_meet(o, rows, y, rows)) ||
+        buffers_meet(o, rows, post_weight, one) || buffers_meet(o, rows, pre_weight, one) ||
+        buffers_meet(o, rows, gate, (uintptr_t)(M - 1) * gate_ld * 2 + one))
       return set_error(SPEAR_ERR_INVALID_ARG, "an output overlaps an input that it is not equal to");
-  if (meet(x_out, rows, h, rows)) return set_error(SPEAR_ERR_INVALID_ARG, "x_out and h overlap");
+  if (buffers_meet(x_out, rows, h, rows)) return set_error(SPEAR_ERR_INVALID_ARG, "x_out and h overlap");
   auto bf = [](const uint16_t* p) { return reinterpret_cast<const __nv_bfloat16*>(p); };
   const NormArgs a = {bf(x), bf(y), bf(post_weight), bf(gate), bf(pre_weight),
                       reinterpret_cast<__nv_bfloat16*>(x_out), reinterpret_cast<__nv_bfloat16*>(h), gate_ld, K,

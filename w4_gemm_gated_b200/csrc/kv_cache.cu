@@ -363,6 +363,8 @@ extern "C" int spear_kv_read(const spear_kv_cache* cache, const int* slots, int 
   if (!k_out || !v_out) return set_error(SPEAR_ERR_INVALID_ARG, "NULL pointer");
   if (!ptr_aligned16(k_out) || !ptr_aligned16(v_out)) return set_error(SPEAR_ERR_ALIGNMENT, "unaligned pointer");
   if ((long long)n * c.heads > (1LL << 31)) return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "n=%d: too many rows", n);
+  const uintptr_t bytes = (uintptr_t)n * c.heads * c.dim * 2;
+  if (buffers_meet(k_out, bytes, v_out, bytes)) return set_error(SPEAR_ERR_INVALID_ARG, "k_out and v_out overlap");
   const unsigned rows = (unsigned)n * c.heads;
   const int step = step_for(rows, c.dim);
   const dim3 grid(blocks_for(rows, c.dim, step), 2);

@@ -28,6 +28,11 @@ __host__ __device__ constexpr int kv_bits(int kind) {
 int check_kv_cache(const spear_kv_cache* c, KvView* out);
 
 inline bool ptr_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether np bytes from p and nq bytes from q share one (NULL: no).
+inline bool buffers_meet(const void* p, uintptr_t np, const void* q, uintptr_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + nq && b < a + np;
+}
 
 // Distance to a page, in 16-byte steps.
 __device__ __forceinline__ long long page_at(uint32_t page, uint32_t step) { return (long long)((uint64_t)page * step); }
