@@ -235,3 +235,17 @@ def test_binding_refuses_host_tensors_and_wrong_types(S):
         S.block_norm(z((2, 64), dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         S.block_norm(z((2, 64)))
+
+
+def test_advance_gives_slots_up_to_the_last_page(S):
+    from types import SimpleNamespace
+
+    from w4_gemm_gated_b200 import decoder
+    table = torch.tensor([[5, 2], [0, 7], [3, 1], [4, 6]], dtype=torch.int32)
+    state = decoder.StepState([SimpleNamespace(page_size=16)], table, torch.tensor([0, 16, 31, 32], dtype=torch.int32),
+                              torch.zeros(4, dtype=torch.int32), None, None)
+    decoder.advance(state)
+    assert state.slots.tolist() == [80, 112, 31, -1] and state.seq_lens.tolist() == [1, 17, 32, 33]
+    decoder.advance(state)
+    assert state.slots.tolist() == [81, 113, -1, -1] and state.seq_lens.tolist() == [2, 18, 33, 34]
+    assert state.slots.dtype == torch.int32

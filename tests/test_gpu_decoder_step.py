@@ -199,3 +199,20 @@ def test_rotation_is_applied_before_the_cache(S):
     decoder.step(layers, x, state, rotate=rotate)
     back, _ = S.kv_read(state.caches[0], state.slots, state.attn_ws)
     assert torch.equal(back.view(2, -1), -seen[0][1]) and seen[0][0].shape == (2, N_Q * HEAD)
+
+
+def test_a_step_past_the_last_page_is_reported(S):
+    from w4_gemm_gated_b200 import decoder
+    _, layers, _ = _model(S, 1)
+    state = decoder.make_state(layers, 2, 16, kind=S.KV_INT8, head_dim=HEAD)
+    state.seq_lens.copy_(torch.tensor([15, 3], dtype=torch.int32))
+    x = bf16_tensor(np.random.default_rng(7).standard_normal((2, WIDTH)))
+    decoder.advance(state)
+    decoder.step(layers, x, state)
+    assert decoder.status(state) == S.OK
+    held = state.caches[0].k.clone()
+    decoder.advance(state)                     # the first sequence's page is full
+    assert state.slots.tolist() == [-1, 16 + 4]
+    decoder.step(layers, x, state)
+    assert decoder.status(state) == S.ERR_DEVICE_CHECK
+    assert torch.equal(state.caches[0].k[0], held[0]) and not torch.equal(state.caches[0].k[1], held[1])

@@ -50,11 +50,13 @@ def make_state(layers: list, n_seqs: int, max_tokens: int, kind: int = S.KV_INT8
 
 
 def advance(state: StepState) -> None:
-    """Count one new token for every sequence and find its slot."""
-    P = state.caches[0].page_size
-    at = state.seq_lens.long()
-    page = state.page_table.gather(1, (at // P).unsqueeze(1)).squeeze(1)
-    state.slots.copy_(page * P + (at % P).to(torch.int32))
+    """Count one new token for every sequence and find its slot.  A token past the
+    sequence's pages has none: it is not cached, and the attention, whose length
+    is then past the table, reports it (`status`)."""
+    P, pages = state.caches[0].page_size, state.page_table.shape[1]
+    at = state.seq_lens
+    page = state.page_table.gather(1, (at // P).clamp(0, pages - 1).long().unsqueeze(1)).squeeze(1)
+    state.slots.copy_(torch.where((at >= 0) & (at < pages * P), page * P + at % P, -1))
     state.seq_lens.add_(1)
 
 
