@@ -300,7 +300,8 @@ int spear_kv_read(const spear_kv_cache* cache, const int* slots, int n, uint16_t
  * ws         device workspace of ws_bytes >= spear_attn_workspace_bytes,
  *            initialised once by spear_workspace_init, of its own: not one
  *            that layer calls use, and not shared by two calls that may run
- *            concurrently.
+ *            concurrently.  Calls for caches of several shapes may take turns
+ *            in one of the largest size.
  * A length outside its range is cut to it and a page number outside the cache
  * leaves its tokens' keys and values zero; both are reported as
  * SPEAR_ERR_DEVICE_CHECK (spear_read_status), and the sequence's results are

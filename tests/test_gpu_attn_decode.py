@@ -211,6 +211,16 @@ def test_same_result_every_time_and_in_a_shared_workspace(S):
         assert torch.equal(a, out) and torch.equal(b, out2)
 
 
+def test_caches_of_several_shapes_take_turns_in_a_workspace(S):
+    shapes = [("bf16", 256, 4), ("int8", 128, 2), ("bf16", 64, 16), ("int4", 256, 8)]
+    filled = [(Filled(S, kind, [9000, 3, 4000], 2, dim, 64, seed=i), group)
+              for i, (kind, dim, group) in enumerate(shapes)]
+    ws = max((S.make_attn_workspace(f.cache, 2 * group) for f, group in filled), key=torch.numel)
+    for _ in range(2):
+        for f, group in filled:
+            _run(S, f, group, seed=9, ws=ws)
+
+
 def test_graphs_that_share_a_workspace_follow_the_lengths(S):
     f = Filled(S, "bf16", [700, 32, 17], 2, 128, 16, seed=18)
     q = _q(3, 8, 128, 9)

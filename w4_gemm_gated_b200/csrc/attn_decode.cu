@@ -234,7 +234,9 @@ struct Cut {
 // int4 of 32 x 4099 with 32 heads 73.0, not 68.4).
 constexpr bool attn_small(int kind, int dim, int nt) { return kind != SPEAR_KV_BF16 && dim < 256 && nt == 1; }
 constexpr int attn_warps(int kind, int dim, int nt) { return attn_small(kind, dim, nt) ? 8 : 4; }
-constexpr int attn_per_sm(int kind, int dim) { return kind == SPEAR_KV_BF16 && dim == 256 ? 1 : 2; }
+constexpr int attn_per_sm(int kind, int dim) {  // at most 2, which the workspace counts on
+  return kind == SPEAR_KV_BF16 && dim == 256 ? 1 : 2;
+}
 
 // Shared memory of a CTA: per warp a ring of stages and the place of a first
 // piece.  227 KB per SM less 1 KB that each CTA takes besides, and 1 KB for the
@@ -1094,8 +1096,11 @@ static AttnPlan plan_attn(const KvView& c, int n_q_heads) {
 
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// Header and counters, which take the same place for every cache, so that calls for
+// caches of several shapes can take turns in one workspace.
+static size_t attn_ws_parts() { return kWsHeaderBytes + up256(3 * 2 * (size_t)device_sm_count() * sizeof(int)); }
 static size_t attn_ws_bytes(const AttnPlan& a) {
-  return kWsHeaderBytes + up256(3 * a.ctas * sizeof(int)) + up256((size_t)a.ctas * 2 * a.piece * sizeof(float));
+  return attn_ws_parts() + up256((size_t)a.ctas * 2 * a.piece * sizeof(float));
 }
 
 template <int KIND, int DIM, int NT>
@@ -1192,7 +1197,7 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.hdr = reinterpret_cast<WsHeader*>(w);
   a.tickets = reinterpret_cast<int*>(w + kWsHeaderBytes);
-  a.parts = reinterpret_cast<float*>(w + kWsHeaderBytes + up256(3 * pl.ctas * sizeof(int)));
+  a.parts = reinterpret_cast<float*>(w + attn_ws_parts());
   a.ctas = pl.ctas;
   cudaError_t e = cudaErrorInvalidValue;
   for_kind_dim(a.c.kind, a.c.dim, [&](auto kc, auto dc) {

@@ -455,7 +455,8 @@ def attn_workspace_bytes(cache: KVCache, n_q_heads: int) -> int:
 
 
 def make_attn_workspace(cache: KVCache, n_q_heads: int, stream=None) -> torch.Tensor:
-    """A workspace for attn_decode (any batch), kv_write and kv_read on this cache or others of its shape."""
+    """A workspace for attn_decode (any batch), kv_write and kv_read on this cache,
+    and on others, in turn, whose attn_workspace_bytes are no more."""
     n = attn_workspace_bytes(cache, n_q_heads)
     with torch.cuda.device(cache.index), torch.cuda.stream(stream):
         ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
