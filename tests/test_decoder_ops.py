@@ -249,3 +249,12 @@ def test_advance_gives_slots_up_to_the_last_page(S):
     decoder.advance(state)
     assert state.slots.tolist() == [81, 113, -1, -1] and state.seq_lens.tolist() == [2, 18, 33, 34]
     assert state.slots.dtype == torch.int32
+
+
+def test_a_cache_keeps_its_tensors(S):
+    # its struct holds their addresses
+    k, v = (torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16) for _ in range(2))
+    cache = S.KVCache(S.KV_BF16, 2, 16, 1, 64, k, v)
+    with pytest.raises(AttributeError):
+        cache.k = torch.zeros_like(k)
+    assert cache.k is k and cache.struct.k == k.data_ptr() and cache.struct.page_stride == 16 * 64 * 2

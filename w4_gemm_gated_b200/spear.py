@@ -347,11 +347,11 @@ def read_status(ws: torch.Tensor, stream=None) -> int:
 _KV_DTYPES = {torch.bfloat16: KV_BF16, torch.int8: KV_INT8, torch.uint8: KV_INT4}
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class KVCache:
     """Paged key-value cache on the device (keeps its tensors alive; the
     layouts are ``spear_kv_cache``'s).  Make it with :func:`make_kv_cache` or
-    :func:`kv_cache_from_parts`."""
+    :func:`kv_cache_from_parts`; it stays over the tensors it was made with."""
 
     kind: int
     n_pages: int
@@ -365,13 +365,14 @@ class KVCache:
 
     def __post_init__(self):
         quant = self.kind != KV_BF16
-        self.device, self.index = self.k.device, self.k.get_device()
-        self.struct = KVCacheStruct(
+        struct = KVCacheStruct(
             self.kind, self.n_pages, self.page_size, self.n_heads, self.head_dim, self.k.data_ptr(), self.v.data_ptr(),
             self.k_scales.data_ptr() if quant else None, self.v_scales.data_ptr() if quant else None,
             self.k.stride(0) * self.k.element_size() if self.n_pages > 1 else 0,
             self.k_scales.stride(0) if quant and self.n_pages > 1 else 0)
-        self.address = ctypes.addressof(self.struct)
+        for name, value in (("device", self.k.device), ("index", self.k.get_device()), ("struct", struct),
+                            ("address", ctypes.addressof(struct))):
+            object.__setattr__(self, name, value)
 
 
 def _dense_pages(t: torch.Tensor) -> bool:
