@@ -93,24 +93,31 @@ class Filled:
         G = H // self.heads
         for b, n in enumerate(self.lens):
             o, l, p = O.attend(q[b], self.k[b], self.v[b], scale)
-            # the score's sum of D products and its scalings in 32 bits.  Codes of
-            # 4 bits enter as 128 + u, u = c + 8 in 1..15, with 136 q subtracted from
-            # their sum: the terms are up to 143 s |q| then, and their sum as large
+            # The score's error.  bf16: a sum of D products in 32 bits and its scalings.
+            # Codes enter as 1024 + u (or 64 + u), u up to 255 or 15, and the sum starts at
+            # minus what that adds: terms up to 1279 s |q| (1039 s |q|) and a start as
+            # large, in D / 16 products whose sums are each off by a step of 32 bits
+            # (2^-23) at most, and two scalings.  No scale s is above max|k| / Q (1 + 2^-11).
             ds = 0.0
             if n:
-                s4 = np.abs(self.k[b]).max(axis=(0, 2)) / 7.0          # no scale is larger (7 s >= max)
-                kk = np.abs(self.k[b]).max(axis=0)                     # G x D
-                big = kk + (143.0 * 1.01 * s4[:, None] * 2 if self.kind == "int4" else 0.0)
-                ds = abs(scale) * np.max(np.sum(np.abs(q[b]) * np.repeat(big, G, axis=0), axis=-1)) * (D + 8) * 2.0 ** -24
-            # weights off by the score's error and the exponential's (2^-21), each rounded
-            # once to bf16 with its value's scale, products summed in 32 bits (as many
-            # roundings as tokens at most, of partial sums of the magnitudes)
+                sum_q = np.sum(np.abs(q[b]), axis=-1)                              # H
+                if self.kind == "bf16":
+                    kk = np.repeat(np.abs(self.k[b]).max(axis=0), G, axis=0)       # H x D
+                    ds = np.max(np.sum(np.abs(q[b]) * kk, axis=-1)) * (D + 8) * 2.0 ** -24
+                else:
+                    top, Q = (1279, 127) if self.kind == "int8" else (1039, 7)
+                    s = np.repeat(np.abs(self.k[b]).max(axis=(0, 2)), G) / Q * 1.01    # H
+                    ds = np.max(sum_q * s) * 2 * top * (D / 16 + 2) * 2.0 ** -23
+                ds *= abs(scale)
+            # Weights off by the score's error and the exponential's (2^-20), each rounded
+            # to two bf16 parts (2^-17), or with its value's scale to fp16 (2^-11, and
+            # where it is under 2^-25 of the largest, to 2^-36 of that); products summed in
+            # 32 bits (as many roundings as tokens at most, of partial sums of the magnitudes).
             pv = np.stack([p[h] @ np.abs(self.v[b][:, h // G]) for h in range(H)]) if n else np.zeros((H, D))
-            pmag = pv
-            if self.kind == "int4" and n:
-                pmag = np.stack([p[h] @ np.repeat(np.abs(self.v[b][:, h // G]).max(-1)[:, None] / 7 * 1.01, D, 1)
-                                 for h in range(H)]) * 286.0           # 143 and its subtraction
-            tol_o.append(HALF * np.abs(o) + (HALF + 2 * ds + 2.0 ** -20) * pv + pmag * min(n + 16, 4096) * 2.0 ** -24
+            rounding, lost = 2.0 ** -17, 0.0
+            if self.kind != "bf16":
+                rounding, lost = 2.0 ** -11, n * 2.0 ** -36 * (np.abs(self.v[b]).max() if n else 0.0)
+            tol_o.append(HALF * np.abs(o) + (rounding + 2 * ds + 2.0 ** -20 + min(n + 16, 4096) * 2.0 ** -24) * pv + lost
                          + 1e-30)
             tol_l.append(np.full(H, ds + 2.0 ** -20) + 2.0 ** -22 * np.where(np.isfinite(l), np.abs(l), 0) +
                          (n + 16) * 2.0 ** -24)

@@ -30,8 +30,9 @@
 // 2^-11, under a quarter of the output's own rounding), which the reference,
 // taken of the products, keeps in its range.  The sum in the denominator is of
 // the unrounded weights.  int8 and int4 codes become fp16 as 1024 + u or 1024 + 16 u,
-// exact, and what they are too large by is taken off in fp32: by what the sums
-// start from (scores), at the end (int8) or with every product (int4).
+// exact.  What they are too large by the scores' sums start from, negative; for the
+// output it is taken off the operand, exactly, as sums that cancel would lose the
+// small weights' bits.
 //
 // Joining.  A warp whose run starts or ends inside a unit leaves (maximum, sum,
 // output) in shared memory; the CTA joins the pieces of a unit in order, and
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
     for (int b = 0; b < TS; ++b) {
       if (WHOLE || 16 * b < rows) {
-        float f0 = 1.f, f1 = 1.f;
+        [[maybe_unused]] float f0 = 1.f, f1 = 1.f;
         if constexpr (L::QUANT) {
           f0 = sv[b][0], f1 = sv[b][1];
           if (!WHOLE) {  // scales of rows past the end may be anything
@@ -719,7 +720,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
             if (16 * b + r1 >= rows) f1 = 0.f;
           }
         }
-        uint32_t pb[NT][2], pl[NT][2];
+        uint32_t pb[NT][2];
+        [[maybe_unused]] uint32_t pl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float e[4];
@@ -770,10 +772,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
               }
             } else if constexpr (KIND == SPEAR_KV_INT8) {
               const uint32_t l01 = lo01 ^ kFlip, h01 = hi01 ^ kFlip, l89 = lo89 ^ kFlip, h89 = hi89 ^ kFlip;
-              const uint32_t a[4] = {sub2(bytes_f16<0x5250>(l01), kOff1152), sub2(bytes_f16<0x5351>(l01), kOff1152), sub2(bytes_f16<0x5250>(l89), kOff1152),
-                                     sub2(bytes_f16<0x5351>(l89), kOff1152)};
-              const uint32_t c[4] = {sub2(bytes_f16<0x5250>(h01), kOff1152), sub2(bytes_f16<0x5351>(h01), kOff1152), sub2(bytes_f16<0x5250>(h89), kOff1152),
-                                     sub2(bytes_f16<0x5351>(h89), kOff1152)};
+              const uint32_t a[4] = {sub2(bytes_f16<0x5250>(l01), kOff1152), sub2(bytes_f16<0x5351>(l01), kOff1152),
+                                     sub2(bytes_f16<0x5250>(l89), kOff1152), sub2(bytes_f16<0x5351>(l89), kOff1152)};
+              const uint32_t c[4] = {sub2(bytes_f16<0x5250>(h01), kOff1152), sub2(bytes_f16<0x5351>(h01), kOff1152),
+                                     sub2(bytes_f16<0x5250>(h89), kOff1152), sub2(bytes_f16<0x5351>(h89), kOff1152)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma<true>(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
@@ -784,8 +786,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
               for (int h = 0; h < 2; ++h) {
                 const uint32_t l01 = h ? lo01 >> 8 : lo01, l89 = h ? lo89 >> 8 : lo89;
                 const uint32_t h01 = h ? hi01 >> 8 : hi01, h89 = h ? hi89 >> 8 : hi89;
-                const uint32_t a[4] = {sub2(low4_f16(l01), kOff1032), sub2(high4_f16(l01), kOff1152), sub2(low4_f16(l89), kOff1032), sub2(high4_f16(l89), kOff1152)};
-                const uint32_t c[4] = {sub2(low4_f16(h01), kOff1032), sub2(high4_f16(h01), kOff1152), sub2(low4_f16(h89), kOff1032), sub2(high4_f16(h89), kOff1152)};
+                const uint32_t a[4] = {sub2(low4_f16(l01), kOff1032), sub2(high4_f16(l01), kOff1152),
+                                       sub2(low4_f16(l89), kOff1032), sub2(high4_f16(l89), kOff1152)};
+                const uint32_t c[4] = {sub2(low4_f16(h01), kOff1032), sub2(high4_f16(h01), kOff1152),
+                                       sub2(low4_f16(h89), kOff1032), sub2(high4_f16(h89), kOff1152)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   mma<true>(acc[a0 + h][nt], a, pb[nt][0], pb[nt][1]);
