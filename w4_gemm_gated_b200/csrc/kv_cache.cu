@@ -59,9 +59,9 @@ __device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t w) { return __v
 // chunks of 8 values that lie DIM / 2 apart (so that every load and store of a
 // warp is of whole sectors).  At large sizes both calls are as near the issue
 // rate as HBM, so what a row costs beside its values is spread over 16 of them (8
-// per lane: 40.5 us to read back where it is 33.0, 18.0 to write where it is 11.5).
+// per lane took 1.2 times as long to read back, 1.6 times to write).
 // 29,300 tokens of 8 int8 heads are read back in 31.7 us, 87 % of what a copy of as
-// many bytes reaches, 7,200 written in 11.2 us, 60 % (of bf16 heads 96 and 84 %).
+// many bytes reaches, 7,200 written in 10.3 us, 66 % (of bf16 heads 96 and 84 %).
 constexpr int kThreads = 256;
 
 // Token and head of a row.  magic = floor(2^32 / heads): the product's high half is
@@ -86,6 +86,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -96,29 +101,28 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 //
 // x has 8 significant bits and s 11, so a quotient of at most 128 that is no tie
 // (k + 1/2) is at least 1 / (2 * 2047) = 2.4e-4 away from one; x * (1 / s), with a
-// reciprocal of up to 2 ulp, is within 2^-21.6 * 128 = 4e-5 of it.  Rounded to a
-// multiple of 2^-13 (by adding 1.5 * 2^10, where that is the spacing; off by 6.1e-5
+// reciprocal of up to 2 ulp, is within 2^-22 * 128 = 3.1e-5 of it.  Rounded once to a
+// multiple of 2^-13 (with 1.5 * 2^10 added, where that is the spacing; off by 6.1e-5
 // more at most), a tie becomes the tie exactly and nothing else does, and rounding
-// that to an integer (by adding 1.5 * 2^23, whose low byte then holds it) is the
-// definition's.
+// that to an integer (with 1.5 * 2^23 in the other's place, whose low byte then
+// holds it) is the definition's.
 // clamp: the row's scale was cut or is below fp16's normal range, so that
 // quotients pass Q (elsewhere they stay under Q (1 + 2^-11), which rounds to Q).
 template <int Q>
 __device__ __forceinline__ void quantize8(const uint4& in, float inv, bool clamp, uint32_t& lo, uint32_t& hi) {
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-  const uint64_t inv2 = pair(inv, inv), grid = pair(1536.f, 1536.f), ungrid = pair(-1536.f, -1536.f),
-                 whole = pair(12582912.f, 12582912.f);
+  constexpr float kGrid = 1536.f, kWhole = 12582912.f;
+  const uint64_t inv2 = pair(inv, inv), grid = pair(kGrid, kGrid), whole = pair(kWhole - kGrid, kWhole - kGrid);
   uint32_t y[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint64_t t = mul2(pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), inv2);
-    if (clamp) {
-      float a, b;
-      unpair(t, a, b);
-      t = pair(fminf(fmaxf(a, (float)-Q), (float)Q), fminf(fmaxf(b, (float)-Q), (float)Q));
-    }
+    uint64_t t = fma2(pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), inv2, grid);
     float a, b;
-    unpair(add2(add2(add2(t, grid), ungrid), whole), a, b);
+    if (clamp) {
+      unpair(t, a, b);
+      t = pair(fminf(fmaxf(a, kGrid - Q), kGrid + Q), fminf(fmaxf(b, kGrid - Q), kGrid + Q));
+    }
+    unpair(add2(t, whole), a, b);
     y[2 * i] = __float_as_uint(a);
     y[2 * i + 1] = __float_as_uint(b);
   }
