@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t w) { return __v
 // rate as HBM, so what a row costs beside its values is spread over 16 of them (8
 // per lane took 1.2 times as long to read back, 1.6 times to write).
 // 29,300 tokens of 8 int8 heads are read back in 31.7 us, 87 % of what a copy of as
-// many bytes reaches, 7,200 written in 10.3 us, 66 % (of bf16 heads 96 and 84 %).
+// many bytes reaches, 7,200 written in 9.9 us, 68 % (of bf16 heads 96 and 84 %).
 constexpr int kThreads = 256;
 
 // Token and head of a row.  magic = floor(2^32 / heads): the product's high half is
@@ -144,7 +144,8 @@ __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[WOR
   }
 }
 
-template <int KIND, int DIM>
+// STEP rows per thread, whose loads are in flight together.
+template <int KIND, int DIM, int STEP>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constant__ KvView c,
                                                             const __nv_bfloat16* k, long long ld_k,
                                                             const __nv_bfloat16* v, long long ld_v,
@@ -153,66 +154,77 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
   constexpr int LPR = DIM / 16, RPS = kThreads / LPR, BYTES = kv_bits(KIND);  // bytes of 8 values
   const bool is_v = blockIdx.y != 0;
   const int lane_r = threadIdx.x % LPR;
-  const unsigned row = blockIdx.x * RPS + threadIdx.x / LPR;
-  unsigned tok, head;
-  split_row(row, c.heads, magic, tok, head);
+  const unsigned row0 = blockIdx.x * (STEP * RPS) + threadIdx.x / LPR;
   after_previous();
-  int slot = -1;
-  uint4 in[2] = {};
-  if (row < rows) {
-    slot = slots[tok];
-    const __nv_bfloat16* x = (is_v ? v : k) + tok * (is_v ? ld_v : ld_k) + head * DIM + lane_r * 8;
-    in[0] = *reinterpret_cast<const uint4*>(x);
-    in[1] = *reinterpret_cast<const uint4*>(x + DIM / 2);
+  int slot[STEP];
+  unsigned head[STEP];
+  uint4 in[STEP][2];
+#pragma unroll
+  for (int u = 0; u < STEP; ++u) {
+    const unsigned row = row0 + u * RPS;
+    unsigned tok;
+    split_row(row, c.heads, magic, tok, head[u]);
+    slot[u] = -1;
+    in[u][0] = in[u][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < rows) {
+      slot[u] = slots[tok];
+      const __nv_bfloat16* x = (is_v ? v : k) + tok * (is_v ? ld_v : ld_k) + head[u] * DIM + lane_r * 8;
+      in[u][0] = *reinterpret_cast<const uint4*>(x);
+      in[u][1] = *reinterpret_cast<const uint4*>(x + DIM / 2);
+    }
   }
-  const int page = slot >> c.log_page;
-  const bool live = slot >= 0 && page < c.n_pages;
-  if (slot >= 0 && !live && lane_r == 0) report_status(hdr, SPEAR_ERR_DEVICE_CHECK);
-  const int prow = (head << c.log_page) + (slot & (c.page_size - 1));  // row inside the page
-  uint8_t* dst = (is_v ? c.v : c.k) + (page_at(live ? page : 0, c.page_step) << 4) +
-                 (long long)prow * (DIM / 8 * BYTES) + lane_r * BYTES;
-  if constexpr (KIND == SPEAR_KV_BF16) {
-    if (live) {
-      *reinterpret_cast<uint4*>(dst) = in[0];
-      *reinterpret_cast<uint4*>(dst + DIM / 16 * BYTES) = in[1];
-    }
-  } else {
-    constexpr int Q = KIND == SPEAR_KV_INT8 ? 127 : 7;
-    // max of the magnitudes as 16-bit patterns: a NaN's pattern is above infinity's
-    uint32_t m2 = 0u;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) m2 = absmax2(absmax2(absmax2(absmax2(m2, in[h].x), in[h].y), in[h].z), in[h].w);
-    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-#pragma unroll
-    for (int d = LPR / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d, LPR));
-    __half hs = __float2half_rn(__uint_as_float(m << 16) / (float)Q);
-    if (__hisinf(hs)) hs = __float2half_rn(65504.f);
-    float sf = __half2float(hs);
-    const bool zero = sf == 0.f || sf != sf;  // codes 0: nothing there, or a NaN that the scale keeps
-    if (sf == 0.f) hs = __float2half_rn(1.f);
-    if (zero) sf = 1.f;
-    const float inv = __fdividef(1.f, sf);
-    const bool clamp = __any_sync(0xFFFFFFFFu, sf < 6.103515625e-5f || sf >= 65504.f || zero);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t lo, hi;
-      quantize8<Q>(in[h], inv, clamp, lo, hi);
-      if (zero) lo = hi = 0u;
-      uint8_t* d = dst + h * (DIM / 16 * BYTES);
-      if constexpr (KIND == SPEAR_KV_INT8) {
-        if (live) *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
-      } else {
-        // codes + 8 in the low half of each byte; neighbours into one byte
-        lo = __vadd4(lo, 0x08080808u), hi = __vadd4(hi, 0x08080808u);
-        lo = (lo | lo >> 4) & 0x00FF00FFu, hi = (hi | hi >> 4) & 0x00FF00FFu;
-        if (live) *reinterpret_cast<uint32_t*>(d) = __byte_perm(lo, hi, 0x6420);
+  for (int u = 0; u < STEP; ++u) {
+    const int page = slot[u] >> c.log_page;
+    const bool live = slot[u] >= 0 && page < c.n_pages;
+    if (slot[u] >= 0 && !live && lane_r == 0) report_status(hdr, SPEAR_ERR_DEVICE_CHECK);
+    const int prow = (head[u] << c.log_page) + (slot[u] & (c.page_size - 1));  // row inside the page
+    uint8_t* dst = (is_v ? c.v : c.k) + (page_at(live ? page : 0, c.page_step) << 4) +
+                   (long long)prow * (DIM / 8 * BYTES) + lane_r * BYTES;
+    if constexpr (KIND == SPEAR_KV_BF16) {
+      if (live) {
+        *reinterpret_cast<uint4*>(dst) = in[u][0];
+        *reinterpret_cast<uint4*>(dst + DIM / 16 * BYTES) = in[u][1];
       }
+    } else {
+      constexpr int Q = KIND == SPEAR_KV_INT8 ? 127 : 7;
+      // max of the magnitudes as 16-bit patterns: a NaN's pattern is above infinity's
+      uint32_t m2 = 0u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        m2 = absmax2(absmax2(absmax2(absmax2(m2, in[u][h].x), in[u][h].y), in[u][h].z), in[u][h].w);
+      uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+#pragma unroll
+      for (int d = LPR / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d, LPR));
+      __half hs = __float2half_rn(__uint_as_float(m << 16) / (float)Q);
+      if (__hisinf(hs)) hs = __float2half_rn(65504.f);
+      float sf = __half2float(hs);
+      const bool zero = sf == 0.f || sf != sf;  // codes 0: nothing there, or a NaN that the scale keeps
+      if (sf == 0.f) hs = __float2half_rn(1.f);
+      if (zero) sf = 1.f;
+      const float inv = __fdividef(1.f, sf);
+      const bool clamp = __any_sync(0xFFFFFFFFu, sf < 6.103515625e-5f || sf >= 65504.f || zero);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t lo, hi;
+        quantize8<Q>(in[u][h], inv, clamp, lo, hi);
+        if (zero) lo = hi = 0u;
+        uint8_t* d = dst + h * (DIM / 16 * BYTES);
+        if constexpr (KIND == SPEAR_KV_INT8) {
+          if (live) *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+        } else {
+          // codes + 8 in the low half of each byte; neighbours into one byte
+          lo = __vadd4(lo, 0x08080808u), hi = __vadd4(hi, 0x08080808u);
+          lo = (lo | lo >> 4) & 0x00FF00FFu, hi = (hi | hi >> 4) & 0x00FF00FFu;
+          if (live) *reinterpret_cast<uint32_t*>(d) = __byte_perm(lo, hi, 0x6420);
+        }
+      }
+      if (live && lane_r == 0) (is_v ? c.vs : c.ks)[(page_at(page, c.scale_step) << 3) + prow] = hs;
     }
-    if (live && lane_r == 0) (is_v ? c.vs : c.ks)[(page_at(page, c.scale_step) << 3) + prow] = hs;
   }
 }
 
-// STEP rows per thread taken together, so that their loads are in flight together.
+// As above, back.
 template <int KIND, int DIM, int STEP>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvView c,
                                                            const int* slots, unsigned rows,
@@ -306,9 +318,9 @@ static int blocks_for(long long rows, int dim, int step) {
   return (int)((rows + per - 1) / per);
 }
 
-// Rows per thread when reading back: one while the blocks are few, where only a
+// Rows per thread: one while the blocks are few, where only a
 // call's latency counts (330 tokens of 8 int8 heads: 1.85 us, 2.3 with two), two
-// beyond (29,300: 31.7 us, 33.4 with one; four were 10 % slower than two).
+// beyond (29,300: 31.7 us, 33.4 with one; 7,200 written: 9.9 us, 10.3 with one).
 static int step_for(long long rows, int dim) { return blocks_for(rows, dim, 1) <= 4 * device_sm_count() ? 1 : 2; }
 
 static unsigned magic_for(int heads) { return (unsigned)((1ull << 32) / heads); }
@@ -345,10 +357,12 @@ extern "C" int spear_kv_write(const spear_kv_cache* cache, const uint16_t* k, lo
     return set_error(SPEAR_ERR_INVALID_ARG, "ld_k=%lld ld_v=%lld: multiples of 8 of at least %lld", ld_k, ld_v, row);
   if ((long long)n * c.heads > (1LL << 31)) return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "n=%d: too many rows", n);
   const unsigned rows = (unsigned)n * c.heads;
-  const dim3 grid(blocks_for(rows, c.dim, 1), 2);
+  const int step = step_for(rows, c.dim);
+  const dim3 grid(blocks_for(rows, c.dim, step), 2);
   cudaError_t e = cudaErrorInvalidValue;
   for_kind_dim(c.kind, c.dim, [&](auto kc, auto dc) {
-    e = launch_after(kv_write_kernel<kc.value, dc.value>, grid, kThreads, 0, static_cast<cudaStream_t>(stream), c,
+    auto* f = step == 1 ? kv_write_kernel<kc.value, dc.value, 1> : kv_write_kernel<kc.value, dc.value, 2>;
+    e = launch_after(f, grid, kThreads, 0, static_cast<cudaStream_t>(stream), c,
                      reinterpret_cast<const __nv_bfloat16*>(k), ld_k, reinterpret_cast<const __nv_bfloat16*>(v), ld_v,
                      slots, rows, magic_for(c.heads), static_cast<WsHeader*>(ws));
   });
