@@ -98,6 +98,31 @@ def test_write_and_read_back(S, kind, dim, heads, page, n):
 
 
 @pytest.mark.parametrize("kind", ["int8", "int4"])
+def test_every_maximum_and_its_ties(S, kind):
+    # a row for every finite bf16 magnitude as the row's largest; below it values of the
+    # next eight octaves, and those next to and on the halves between codes
+    rng = np.random.default_rng(6)
+    top = np.arange(0x7F80, dtype=np.int64)[:, None]
+    bits = np.maximum(top - rng.integers(0, 0x400, (0x7F80, 64)), 0)
+    with np.errstate(over="ignore"):
+        s = O.kv_quantize(O.bf16_to_f64(top.astype(np.uint16))[:, None], kind)[1].astype(np.float64)
+    halves = (rng.integers(0, 127 if kind == "int8" else 7, (0x7F80, 32)) + 0.5) * s.reshape(-1, 1)
+    half_bits = O.f32_to_bf16_bits_rne(halves.astype(np.float32)).astype(np.int64) + rng.integers(-1, 2, (0x7F80, 32))
+    bits[:, 32:] = np.clip(half_bits, 0, top)
+    bits[:, 0] = top[:, 0]
+    signed = (bits | rng.integers(0, 2, bits.shape) << 15).astype(np.uint16)
+    x = torch.from_numpy(signed.view(np.int16)).view(torch.bfloat16).view(0x7F80, 1, 64).cuda()
+    cache = S.make_kv_cache(KINDS[kind], 0x7F80 // 64, 64, 1, 64)
+    slots = torch.arange(0x7F80, dtype=torch.int32, device="cuda")
+    ws = _ws(S)
+    S.kv_write(cache, x, x, slots, ws)
+    want, sc, _ = _expected(x, kind)
+    for codes, got in _read_pages(cache, kind, slots.long()):
+        assert torch.equal(codes, want)
+        assert torch.equal(got.view(torch.int16), sc.view(torch.int16))
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
 def test_many_ordinary_rows_bit_for_bit(S, kind):
     # enough quotients that some lie next to a tie
     g = torch.Generator(device="cuda").manual_seed(3)
