@@ -94,10 +94,10 @@ class Filled:
         for b, n in enumerate(self.lens):
             o, l, p = O.attend(q[b], self.k[b], self.v[b], scale)
             # The score's error.  bf16: a sum of D products in 32 bits and its scalings.
-            # Codes enter as 1024 + u (or 64 + u), u up to 255 or 15, and the sum starts at
-            # minus what that adds: terms up to 1279 s |q| (1039 s |q|) and a start as
-            # large, in D / 16 products whose sums are each off by a step of 32 bits
-            # (2^-23) at most, and two scalings.  No scale s is above max|k| / Q (1 + 2^-11).
+            # Codes enter as u = c + 128 or c + 8, and the sum starts at minus what that
+            # adds: terms up to 255 s |q| (15 s |q|) and a start of up to 128 (8) of them,
+            # in D / 16 products whose sums are each off by a step of 32 bits (2^-23) at
+            # most, and three scalings.  No scale s is above max|k| / Q (1 + 2^-11).
             ds = 0.0
             if n:
                 sum_q = np.sum(np.abs(q[b]), axis=-1)                              # H
@@ -105,9 +105,9 @@ class Filled:
                     kk = np.repeat(np.abs(self.k[b]).max(axis=0), G, axis=0)       # H x D
                     ds = np.max(np.sum(np.abs(q[b]) * kk, axis=-1)) * (D + 8) * 2.0 ** -24
                 else:
-                    top, Q = (1279, 127) if self.kind == "int8" else (1039, 7)
+                    top, Q = (255, 127) if self.kind == "int8" else (15, 7)
                     s = np.repeat(np.abs(self.k[b]).max(axis=(0, 2)), G) / Q * 1.01    # H
-                    ds = np.max(sum_q * s) * 2 * top * (D / 16 + 2) * 2.0 ** -23
+                    ds = np.max(sum_q * s) * 2 * top * (D / 16 + 3) * 2.0 ** -23
                 ds *= abs(scale)
             # Weights off by the score's error and the exponential's (2^-20), each rounded
             # to two bf16 parts (2^-17), or with its value's scale to fp16 (2^-11, and

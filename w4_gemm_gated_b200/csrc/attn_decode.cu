@@ -6,7 +6,7 @@
 // operations per value and head), so HBM bounds it in principle, and does for
 // bf16: 2 sequences of up to 131,072 tokens, 8 heads of 128, 800 MB in 128 us, 6.2
 // TB/s.  Quantised caches take a few instructions per code, which bound them where
-// no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 68 us, 4.0 TB/s at 58 %
+// no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 67 us, 4.1 TB/s at 58 %
 // of the issue rate).  Short batches are bound by the chain from the lengths over
 // the page table to the data and by the joins (int8, 16 x 2048: 36 MB in 17 us).
 //
@@ -15,11 +15,11 @@
 // (with a step for each unit besides), which is cut into equal runs, one per CTA
 // and in it one per warp, by the lengths alone (every CTA sums them up): ragged
 // batches load the machine evenly, a long sequence is spread over many warps, and
-// a warp takes many short ones without meeting anybody.  Where every unit is short the CTAs'
-// borders move to units' borders (see Cut).  A warp streams its run through its own ring of shared-memory
-// stages (16-byte asynchronous copies, rows past a sequence's end filled with
-// zeros), so that copies cross the units' borders and never wait for another
-// warp.
+// a warp takes many short ones without meeting anybody.  Where every unit is short
+// the CTAs' borders move to units' borders.  A warp streams its run through its own
+// ring of shared-memory stages (16-byte asynchronous copies, rows past a sequence's
+// end filled with zeros), so that copies cross the units' borders and never wait
+// for another warp.
 //
 // Arithmetic.  Tensor-core products over 16 tokens with the query heads as the 8
 // columns: S = K q (rows: tokens), then O^T += V^T P with P's layout turned by
@@ -27,12 +27,13 @@
 // two; they are rescaled only when a weight passes the reference by 2^kSlack.
 // The operands of the second product are the weights times their values' scales:
 // as two bf16 parts for a bf16 cache; for a quantised one as fp16 (relative
-// 2^-11, under a quarter of the output's own rounding), which the reference,
+// 2^-11, an eighth of the output's own rounding), which the reference,
 // taken of the products, keeps in its range.  The sum in the denominator is of
-// the unrounded weights.  int8 and int4 codes become fp16 as 1024 + u or 1024 + 16 u,
-// exact.  What they are too large by the scores' sums start from, negative; for the
-// output it is taken off the operand, exactly, as sums that cancel would lose the
-// small weights' bits.
+// the unrounded weights.  Codes with an offset, u = c + 128 or c + 8, are
+// fp16 as they are: the subnormals 2^-24 u (2^-24 16 u).  What they are too large by
+// the scores' sums start from, negative; for the output it is taken off the
+// operand, exactly: off the sums it is hardly faster (int4, 32 x 4099, 32 heads: 66.6
+// us, not 67.0) and loses the small weights' bits where large ones meet codes of 0.
 //
 // Joining.  A warp whose run starts or ends inside a unit leaves (maximum, sum,
 // output) in shared memory; the CTA joins the pieces of a unit in order, and
@@ -106,11 +107,6 @@ __device__ __forceinline__ float exp2_(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
-  uint32_t v;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(a), "r"(m), "r"(o));  // (a & m) | o
-  return v;
-}
 __device__ __forceinline__ float log2_(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -130,25 +126,26 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else mma_bf16_16816(d, a, b0, b1);
 }
-// Codes as fp16: an integer u < 1024 in the low bits of 1024 (0x6400) is 1024 + u,
-// exactly.  int8 codes, offset to u = c + 128 by kFlip, two bytes of a word at a
-// time; int4 codes u = c + 8 from bits 0-3 as 1024 + u and from bits 4-7, without
-// a shift, as 1024 + 16 u.
-constexpr uint32_t kFlip = 0x80808080u, kMagic = 0x64006400u;
+// Codes as fp16: an integer u < 1024 in the low bits is the subnormal 2^-24 u, exactly.
+// int8 codes, offset to u = c + 128 by kFlip, two bytes of a word at a time; int4
+// codes u = c + 8 from bits 0-3 as 2^-24 u and from bits 4-7, without a shift, as
+// 2^-24 16 u.
+constexpr uint32_t kFlip = 0x80808080u;
+constexpr float kUnit = 16777216.f;  // 2^24
 template <int SEL>
 __device__ __forceinline__ uint32_t bytes_f16(uint32_t w) {
-  return __byte_perm(w, kMagic, SEL);  // 5 and 7 pick 0x64
+  return __byte_perm(w, 0u, SEL);  // 5 and 7 pick 0
 }
-__device__ __forceinline__ uint32_t low4_f16(uint32_t w) { return and_or(w, 0x000F000Fu, kMagic); }
-__device__ __forceinline__ uint32_t high4_f16(uint32_t w) { return and_or(w, 0x00F000F0u, kMagic); }
-// The offsets 1024 + 8 and 1024 + 128 (of 1024 + 16 u too), to take off exactly.
-constexpr uint32_t kOff1032 = 0x64086408u, kOff1152 = 0x64806480u;
+__device__ __forceinline__ uint32_t low4_f16(uint32_t w) { return w & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t high4_f16(uint32_t w) { return w & 0x00F000F0u; }
+// The offsets 8 and 128 (of 16 u too), to take off exactly.
+constexpr uint32_t kOff8 = 0x00080008u, kOff128 = 0x00800080u;
 __device__ __forceinline__ uint32_t sub2(uint32_t u, uint32_t off) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&off));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 // The same negative, as operands.
-constexpr uint32_t kLess1152 = 0xE480E480u, kLess1032 = 0xE408E408u;
+constexpr uint32_t kLess8 = 0x80088008u, kLess128 = 0x80808080u;
 
 // Layout of a unit's tiles in shared memory and in the fragments.
 template <int KIND, int DIM>
@@ -232,7 +229,7 @@ struct Cut {
 // starts or joins (bf16, 64 x 4096: one of 8 warps 108 us, two of 4 101, four of 2
 // 103).  Quantised kinds are bound by their arithmetic and take 16 warps where 128
 // registers do (two of 8; with two of 4 int8 of 16 x 2048 takes 18.1 us, not 17.0, and
-// int4 of 32 x 4099 with 32 heads 73.0, not 68.4).
+// int4 of 32 x 4099 with 32 heads 7 % more).
 constexpr bool attn_small(int kind, int dim, int nt) { return kind != SPEAR_KV_BF16 && dim < 256 && nt == 1; }
 constexpr int attn_warps(int kind, int dim, int nt) { return attn_small(kind, dim, nt) ? 8 : 4; }
 constexpr int attn_per_sm(int kind, int dim) {  // at most 2, which the workspace counts on
@@ -575,8 +572,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
             }
           }
         }
-        const uint32_t even = KIND == SPEAR_KV_INT8 ? kLess1152 : kLess1032;
-        const uint32_t less[4] = {even, even, kLess1152, kLess1152};
+        const uint32_t even = KIND == SPEAR_KV_INT8 ? kLess128 : kLess8;
+        const uint32_t less[4] = {even, even, kLess128, kLess128};
         float sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < DIM / 8; k += 2) mma<true>(sq, less, qf[nt][k], qf[nt][k + 1]);
@@ -645,8 +642,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         float f0 = 1.f, f1 = 1.f;
         if constexpr (L::QUANT) {
           const uint32_t sa = st + 2 * L::SIDE + 32 * b;
-          f0 = lds_half(sa + 2 * r0);
-          f1 = lds_half(sa + 2 * r1);
+          f0 = lds_half(sa + 2 * r0) * kUnit;
+          f1 = lds_half(sa + 2 * r1) * kUnit;
           sv[b][0] = lds_half(sa + 2 * TILE + 2 * r0);
           sv[b][1] = lds_half(sa + 2 * TILE + 2 * r1);
         }
@@ -654,8 +651,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[b][nt][e] *= f0 * q_scale[nt][e];
-            s[b][nt][e + 2] *= f1 * q_scale[nt][e];
+            s[b][nt][e] = s[b][nt][e] * f0 * q_scale[nt][e];
+            s[b][nt][e + 2] = s[b][nt][e + 2] * f1 * q_scale[nt][e];
           }
         if (!WHOLE) {
 #pragma unroll
@@ -772,10 +769,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
               }
             } else if constexpr (KIND == SPEAR_KV_INT8) {
               const uint32_t l01 = lo01 ^ kFlip, h01 = hi01 ^ kFlip, l89 = lo89 ^ kFlip, h89 = hi89 ^ kFlip;
-              const uint32_t a[4] = {sub2(bytes_f16<0x5250>(l01), kOff1152), sub2(bytes_f16<0x5351>(l01), kOff1152),
-                                     sub2(bytes_f16<0x5250>(l89), kOff1152), sub2(bytes_f16<0x5351>(l89), kOff1152)};
-              const uint32_t c[4] = {sub2(bytes_f16<0x5250>(h01), kOff1152), sub2(bytes_f16<0x5351>(h01), kOff1152),
-                                     sub2(bytes_f16<0x5250>(h89), kOff1152), sub2(bytes_f16<0x5351>(h89), kOff1152)};
+              const uint32_t a[4] = {sub2(bytes_f16<0x5250>(l01), kOff128), sub2(bytes_f16<0x5351>(l01), kOff128),
+                                     sub2(bytes_f16<0x5250>(l89), kOff128), sub2(bytes_f16<0x5351>(l89), kOff128)};
+              const uint32_t c[4] = {sub2(bytes_f16<0x5250>(h01), kOff128), sub2(bytes_f16<0x5351>(h01), kOff128),
+                                     sub2(bytes_f16<0x5250>(h89), kOff128), sub2(bytes_f16<0x5351>(h89), kOff128)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma<true>(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
@@ -786,10 +783,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
               for (int h = 0; h < 2; ++h) {
                 const uint32_t l01 = h ? lo01 >> 8 : lo01, l89 = h ? lo89 >> 8 : lo89;
                 const uint32_t h01 = h ? hi01 >> 8 : hi01, h89 = h ? hi89 >> 8 : hi89;
-                const uint32_t a[4] = {sub2(low4_f16(l01), kOff1032), sub2(high4_f16(l01), kOff1152),
-                                       sub2(low4_f16(l89), kOff1032), sub2(high4_f16(l89), kOff1152)};
-                const uint32_t c[4] = {sub2(low4_f16(h01), kOff1032), sub2(high4_f16(h01), kOff1152),
-                                       sub2(low4_f16(h89), kOff1032), sub2(high4_f16(h89), kOff1152)};
+                const uint32_t a[4] = {sub2(low4_f16(l01), kOff8), sub2(high4_f16(l01), kOff128),
+                                       sub2(low4_f16(l89), kOff8), sub2(high4_f16(l89), kOff128)};
+                const uint32_t c[4] = {sub2(low4_f16(h01), kOff8), sub2(high4_f16(h01), kOff128),
+                                       sub2(low4_f16(h89), kOff8), sub2(high4_f16(h89), kOff128)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   mma<true>(acc[a0 + h][nt], a, pb[nt][0], pb[nt][1]);
@@ -833,7 +830,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
           for (int e = 0; e < 2; ++e) {
             const int h = nt * 8 + 2 * cl + e;
             if (h < gn) {
-              const float even = 1.f / l[nt][e], odd = KIND == SPEAR_KV_INT4 ? 0.0625f * even : even;
+              const float even = (L::QUANT ? kUnit : 1.f) / l[nt][e], odd = KIND == SPEAR_KV_INT4 ? 0.0625f * even : even;
               __nv_bfloat16* o = p.out + at.b * p.ld_out + (long long)(h0 + h) * DIM;
 #pragma unroll
               for (int a = 0; a < MT; a += 4) {
@@ -899,7 +896,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         __stcg(part + 8 * NT * DIM + 8 * NT + h, sum);
       }
     } else {
-      const float inv = 1.f / sum;
+      const float inv = (L::QUANT ? kUnit : 1.f) / sum;
       if constexpr (KIND == SPEAR_KV_INT4) o.y *= 0.0625f, o.w *= 0.0625f;  // odd dims, from bits 4-7
       *reinterpret_cast<uint2*>(p.out + pc.b * p.ld_out + (long long)(pc.h0 + h) * DIM + d) =
           make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
