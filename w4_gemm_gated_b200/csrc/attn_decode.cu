@@ -6,7 +6,7 @@
 // operations per value and head), so HBM bounds it in principle, and does for
 // bf16: 2 sequences of up to 131,072 tokens, 8 heads of 128, 800 MB in 128 us, 6.2
 // TB/s.  Quantised caches take a few instructions per code, which bound them where
-// no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 67 us, 4.1 TB/s at 58 %
+// no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 63 us, 4.3 TB/s at 58 %
 // of the issue rate).  Short batches are bound by the chain from the lengths over
 // the page table to the data and by the joins (int8, 16 x 2048: 36 MB in 17 us).
 //
@@ -253,7 +253,8 @@ struct Room {
 
 constexpr int kMaxSeqs = 4096;
 
-template <int KIND, int DIM, int NT, int W, int PER_SM>
+// EH: columns of each lane's pair that can be heads; 1: only even columns are.
+template <int KIND, int DIM, int NT, int EH, int W, int PER_SM>
 __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_constant__ AttnArgs p) {
   using L = Lay<KIND, DIM>;
   using R = Room<KIND, DIM, NT>;
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < EH; ++e) {
             s[b][nt][e] = s[b][nt][e] * f0 * q_scale[nt][e];
             s[b][nt][e + 2] = s[b][nt][e + 2] * f1 * q_scale[nt][e];
           }
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < EH; ++e) {
               if (16 * b + r0 >= rows) s[b][nt][e] = -INFINITY;
               if (16 * b + r1 >= rows) s[b][nt][e + 2] = -INFINITY;
             }
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+          for (int e = 0; e < EH; ++e)
             top[nt][e] = fmaxf(top[nt][e], fmaxf(s[b][nt][e] + g0, s[b][nt][e + 2] + g1));
       }
     }
@@ -680,13 +681,13 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) above |= top[nt][e] > m[nt][e] + (kUp(L::QUANT) + kSlack(L::QUANT));
+      for (int e = 0; e < EH; ++e) above |= top[nt][e] > m[nt][e] + (kUp(L::QUANT) + kSlack(L::QUANT));
     if (__any_sync(ALL, above)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float f[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < EH; ++e) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(ALL, top[nt][e], d));
           const float now = fmaxf(top[nt][e] - kUp(L::QUANT), m[nt][e]);
@@ -697,14 +698,14 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[a][nt][e] *= f[e & 1];
+          for (int e = 0; e < 4; e += 3 - EH) acc[a][nt][e] *= f[e & 1];
       }
     }
     float ref[NT][2];  // scores of -infinity alone leave m there: their weights are 0
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) ref[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+      for (int e = 0; e < EH; ++e) ref[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
     // ---- weights, and O^T += V^T P -----------------------------------------------------------
 #pragma unroll
     for (int b = 0; b < TS; ++b) {
@@ -721,11 +722,11 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         [[maybe_unused]] uint32_t pl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float e[4];
+          float e[4] = {};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) e[k] = exp2_(s[b][nt][k] - ref[nt][k & 1]);
+          for (int k = 0; k < 4; k += 3 - EH) e[k] = exp2_(s[b][nt][k] - ref[nt][k & 1]);
           l[nt][0] += e[0] + e[2];
-          l[nt][1] += e[1] + e[3];
+          if (EH == 2) l[nt][1] += e[1] + e[3];
           if constexpr (L::QUANT) {
             pb[nt][0] = movmatrix(pack_f16x2(e[0] * f0, e[1] * f0));
             pb[nt][1] = movmatrix(pack_f16x2(e[2] * f1, e[3] * f1));
@@ -820,14 +821,14 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < EH; ++e)
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(ALL, l[nt][e], d);
       if (fresh && from == 0) {  // the whole unit: out with it
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < EH; ++e) {
             const int h = nt * 8 + 2 * cl + e;
             if (h < gn) {
               const float even = (L::QUANT ? kUnit : 1.f) / l[nt][e], odd = KIND == SPEAR_KV_INT4 ? 0.0625f * even : even;
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < EH; ++e) {
             const int h = nt * 8 + 2 * cl + e;
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
@@ -1104,12 +1105,12 @@ static size_t attn_ws_bytes(const AttnPlan& a) {
   return attn_ws_parts() + up256((size_t)a.ctas * 2 * a.piece * sizeof(float));
 }
 
-template <int KIND, int DIM, int NT>
+template <int KIND, int DIM, int NT, int EH>
 static cudaError_t launch_attn(AttnArgs& a, const AttnPlan& pl, cudaStream_t st) {
   using L = Lay<KIND, DIM>;
   using R = Room<KIND, DIM, NT>;
   constexpr int W = R::W;
-  auto* k = attn_kernel<KIND, DIM, NT, W, R::PER_SM>;
+  auto* k = attn_kernel<KIND, DIM, NT, EH, W, R::PER_SM>;
   static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1200,14 +1201,22 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   a.tickets = reinterpret_cast<int*>(w + kWsHeaderBytes);
   a.parts = reinterpret_cast<float*>(w + attn_ws_parts());
   a.ctas = pl.ctas;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
   for_kind_dim(a.c.kind, a.c.dim, [&](auto kc, auto dc) {
     if constexpr (dc.value < 256)
       if (pl.nt == 2) {
-        e = launch_attn<kc.value, dc.value, 2>(a, pl, static_cast<cudaStream_t>(stream));
+        e = launch_attn<kc.value, dc.value, 2, 2>(a, pl, st);
         return;
       }
-    e = launch_attn<kc.value, dc.value, 1>(a, pl, static_cast<cudaStream_t>(stream));
+    // One query head per kv head: a lane's second column is none, and its softmax is
+    // left out (int4, 32 x 4099, 32 heads: 63.3 us, 67.0 with it).  bf16 waits for HBM.
+    if constexpr (kc.value != SPEAR_KV_BF16)
+      if (a.group == 1) {
+        e = launch_attn<kc.value, dc.value, 1, 1>(a, pl, st);
+        return;
+      }
+    e = launch_attn<kc.value, dc.value, 1, 2>(a, pl, st);
   });
   return e == cudaSuccess ? SPEAR_OK : set_cuda_error("attention launch", e);
 }
