@@ -307,7 +307,7 @@ int spear_kv_read(const spear_kv_cache* cache, const int* slots, int n, uint16_t
  * SPEAR_ERR_DEVICE_CHECK (spear_read_status), and the sequence's results are
  * then unspecified.  0 <= n_seqs <= 4096 (0: nothing is launched);
  * n_seqs * max_pages * page_size * n_q_heads < 2^35.  The result does not depend on
- * timing: the split over the cache is a function of the lengths alone. */
+ * timing: the split over the cache is a function of the sizes and lengths alone. */
 size_t spear_attn_workspace_bytes(const spear_kv_cache* cache, int n_q_heads);
 int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q, long long ld_q, int n_seqs, int n_q_heads,
                       const int* page_table, int max_pages, int ld_table, const int* seq_lens, float scale,

@@ -57,6 +57,16 @@ def test_groups_past_one_tile(S, group):
     _run(S, f, group, seed=3)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "int8", "int4"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [9, 16, 29])
+def test_wide_groups_over_many_tokens(S, kind, dim, group):
+    # tables that have room for as many tokens as bring pairs of products: short
+    # sequences, none, and one over many CTAs
+    f = Filled(S, kind, [6000, 0, 1, 130], 1, dim, 64, seed=dim + group, max_pages=1500)
+    _run(S, f, group, seed=5)
+
+
 @pytest.mark.parametrize("kind,lens,heads", [
     ("bf16", [5000], 1), ("int8", [3001, 2], 2), ("int4", [2500], 3),      # one long unit over many workers
     ("int8", [40] * 100, 8),                                               # many short ones

@@ -1082,16 +1082,23 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 // host side
 // ---------------------------------------------------------------------------
 struct AttnPlan {
-  int nt, blocks, piece;
-  int ctas;  // at most
+  int nt, blocks;
+  int piece;  // floats of a part, Room::PIECE, at most
+  int ctas;   // at most
 };
 
-static AttnPlan plan_attn(const KvView& c, int n_q_heads) {
+// tokens: of all sequences, at most.  Groups of more than 8 query heads go through
+// two products side by side, which read a tile once, where there are tiles enough;
+// else as units of 8 each, of which twice as many warps run and join smaller parts
+// (heads 48/4 of 128, sequences to 4096; int8: 64 of them 53.7 us, 64.5 as units of
+// 8, 16 of them 24.5, 22.2; bf16: 62.1, 88.5, and 27.8, 26.2; 8 of them 23.3, 18.7).
+static AttnPlan plan_attn(const KvView& c, int n_q_heads, long long tokens) {
   AttnPlan a;
   const int group = n_q_heads / c.heads;
-  a.nt = group > 8 && c.dim < 256 ? 2 : 1;
+  const bool may_pair = group > 8 && c.dim < 256;
+  a.nt = may_pair && tokens * c.heads > 2560LL * device_sm_count() ? 2 : 1;
   a.blocks = (group + 8 * a.nt - 1) / (8 * a.nt);
-  a.piece = (8 * a.nt * (c.dim + 2) + 3) / 4 * 4;  // Room::PIECE
+  a.piece = (8 * (may_pair ? 2 : 1) * (c.dim + 2) + 3) / 4 * 4;
   a.ctas = device_sm_count() * attn_per_sm(c.kind, c.dim);
   return a;
 }
@@ -1138,7 +1145,7 @@ using namespace spear;
 extern "C" size_t spear_attn_workspace_bytes(const spear_kv_cache* cache, int n_q_heads) {
   KvView c;
   if (check_kv_cache(cache, &c) != SPEAR_OK || n_q_heads < 1 || n_q_heads > 1024 || n_q_heads % c.heads) return 0;
-  return attn_ws_bytes(plan_attn(c, n_q_heads));
+  return attn_ws_bytes(plan_attn(c, n_q_heads, 0));
 }
 
 extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q, long long ld_q, int n_seqs,
@@ -1179,7 +1186,7 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
     if (n_seqs == 1 || ld_q != ld_out || column < row || column + row > ld_q)
       return set_error(SPEAR_ERR_INVALID_ARG, "q and out overlap");
   }
-  const AttnPlan pl = plan_attn(a.c, n_q_heads);
+  const AttnPlan pl = plan_attn(a.c, n_q_heads, (long long)n_seqs * max_pages * a.c.page_size);
   const size_t need = attn_ws_bytes(pl);
   if (ws_bytes < need) return set_error(SPEAR_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
