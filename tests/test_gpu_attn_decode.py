@@ -105,6 +105,17 @@ def test_sharp_softmax_and_large_scores(S, kind):
     _run(S, f, 4, seed=7, q_scale=4.0)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "int8", "int4"])
+@pytest.mark.parametrize("power", [-100, -20, 20, 100])
+def test_powers_of_two_between_q_and_scale_change_nothing(S, kind, power):
+    f = Filled(S, kind, [5, 130, 700], 2, 128, 16, seed=4)
+    q = _q(3, 8, 128, 4)
+    ws = S.make_attn_workspace(f.cache, 8)
+    want = S.attn_decode(q, f.cache, f.table, f.seq_lens, ws, scale=0.1)
+    got = S.attn_decode(q * 2.0 ** power, f.cache, f.table, f.seq_lens, ws, scale=0.1 * 2.0 ** -power)
+    assert torch.isfinite(want).all() and torch.equal(got, want)
+
+
 def test_negative_and_zero_scale(S):
     f = Filled(S, "int4", [90], 2, 64, 16, seed=9)
     _run(S, f, 2, seed=8, scale=-0.2)

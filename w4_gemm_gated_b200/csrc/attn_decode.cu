@@ -540,7 +540,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       q_scale[nt][0] = q_scale[nt][1] = p.scale;
       if constexpr (L::QUANT) {
         // to fp16, each head by the power of two that brings its largest value to
-        // 8..16, so that nothing overflows and what is lost is under 2^-28 of it
+        // 2^14..2^15, so that nothing overflows and what is lost (of a sixteenth, for odd
+        // nibbles) is under 2^-34 of it
         uint32_t m2 = 0u;
 #pragma unroll
         for (int k = 0; k < DIM / 8; ++k) m2 = __vmaxu2(m2, qf[nt][k] & 0x7FFF7FFFu);
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         mag = max(mag, __shfl_xor_sync(ALL, mag, 1));
         mag = max(mag, __shfl_xor_sync(ALL, mag, 2));
         const int ex = mag >> 7;  // bf16's exponent field; 0: a zero row
-        const int up = ex == 0 ? 127 : min(257 - ex, 253);
+        const int up = ex == 0 ? 127 : min(268 - ex, 253);
         const float f = __uint_as_float((uint32_t)up << 23);
         const float back = __uint_as_float((uint32_t)(254 - up) << 23);
         q_scale[nt][0] *= __shfl_sync(ALL, back, 8 * cl);
