@@ -330,3 +330,35 @@ def test_binding_refusals(S):
         S.make_attn_workspace(f.cache, 5)
     empty = S.attn_decode(q[:0], f.cache, f.table[:0], f.seq_lens[:0], ws)
     assert empty.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+def test_pages_shared_between_sequences_and_repeated_in_one(S, kind):
+    f = Filled(S, kind, [640, 640, 640], 2, 64, 32, seed=12)
+    f.table[1] = f.table[0]                       # a second reader of the same tokens
+    f.k[1], f.v[1] = f.k[0], f.v[0]
+    f.table[2, 1:] = f.table[2, :1]               # one page for all of a sequence
+    f.k[2], f.v[2] = (np.concatenate([t[2][:32]] * 20) for t in (f.k, f.v))
+    q, out, _, ws = _run(S, f, 3, seed=13)
+    same = q.clone()
+    same[1] = q[0]
+    again = S.attn_decode(same, f.cache, f.table, f.seq_lens, ws)
+    assert torch.equal(again[0], out[0]) and torch.equal(again[2], out[2])
+
+
+def test_two_calls_at_once_on_one_cache(S):
+    f = Filled(S, "int8", [5000, 0, 37, 2100], 2, 128, 16, seed=14)
+    qs = [_q(4, 8, 128, seed) for seed in (15, 16)]
+    wss = [S.make_attn_workspace(f.cache, 8) for _ in qs]
+    want = [S.attn_decode(q, f.cache, f.table, f.seq_lens, ws) for q, ws in zip(qs, wss)]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(S.attn_decode(qs[i], f.cache, f.table, f.seq_lens, wss[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert S.read_status(wss[i]) == S.OK
+        assert all(torch.equal(g, want[i]) for g in got[i])
