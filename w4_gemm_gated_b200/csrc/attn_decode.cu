@@ -6,8 +6,7 @@
 // operations per value and head), so HBM bounds it in principle, and does for
 // bf16: 2 sequences of up to 131,072 tokens, 8 heads of 128, 800 MB in 128 us, 6.2
 // TB/s.  Quantised caches take a few instructions per code, which bound them where
-// no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 63 us, 4.3 TB/s at 58 %
-// of the issue rate).  Short batches are bound by the chain from the lengths over
+// no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 66 us, 4.1 TB/s).  Short batches are bound by the chain from the lengths over
 // the page table to the data and by the joins (int8, 16 x 2048: 36 MB in 17 us).
 //
 // Work.  A unit is one (sequence, kv head) with up to 8 NT query heads; its
@@ -25,15 +24,16 @@
 // columns: S = K q (rows: tokens), then O^T += V^T P with P's layout turned by
 // movmatrix.  Running reference, sum and output of a softmax in fp32, in powers of
 // two; they are rescaled only when a weight passes the reference by 2^kSlack.
-// The operands of the second product are the weights times their values' scales:
-// as two bf16 parts for a bf16 cache; for a quantised one as fp16 (relative
-// 2^-11, an eighth of the output's own rounding), which the reference,
-// taken of the products, keeps in its range.  The sum in the denominator is of
-// the unrounded weights.  Codes with an offset, u = c + 128 or c + 8, are
-// fp16 as they are: the subnormals 2^-24 u (2^-24 16 u).  What they are too large by
-// the scores' sums start from, negative; for the output it is taken off the
-// operand, exactly: off the sums it is hardly faster (int4, 32 x 4099, 32 heads: 66.6
-// us, not 67.0) and loses the small weights' bits where large ones meet codes of 0.
+// The operands of the second product are the weights times their values' scales
+// as two bf16 parts each (relative 2^-17, 2^-9 of the output's own rounding).  One
+// fp16 part costs less (int4, 32 x 4099, 32 heads: 63 us) but has 2^-11, and too short a
+// range: a token of large weight whose values are small or nothing, as padding's are,
+// brings the others, which the output then consists of, among its subnormals.
+// The sum in the denominator is of the unrounded weights.  Codes with an offset, u
+// = c + 128 or c + 8, are subnormals as they are: 2^-24 u (2^-24 16 u) of fp16,
+// beside q, 2^-133 u of bf16, beside the weights.  What they are too large by the
+// scores' sums start from, negative; for the output one product-sum brings the
+// operand to 2^-6 c, exactly.
 //
 // Joining.  A warp whose run starts or ends inside a unit leaves (maximum, sum,
 // output) in shared memory; the CTA joins the pieces of a unit in order, and
@@ -65,11 +65,7 @@ struct AttnArgs {
 
 constexpr int kRadix = 16;    // parts of a unit joined at once; more are joined in groups of as many first
 constexpr int kMinTiles = 2;  // tiles a warp should have before more CTAs take part
-// How far, in powers of two, the largest weight may lie above 1: kept kUp above the
-// reference, up to kSlack more.  fp16 operands (to 65504) are brought to the top of
-// their range, where weights down to 2^-25 of the largest keep all their bits.
-constexpr float kUp(bool f16) { return f16 ? 11.f : 0.f; }
-constexpr float kSlack(bool f16) { return f16 ? 4.f : 8.f; }
+constexpr float kSlack = 8.f;  // how far, in powers of two, a weight may lie above 1
 constexpr int kShort = 32;    // tiles up to which a unit stays in one CTA
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -107,11 +103,6 @@ __device__ __forceinline__ float exp2_(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float log2_(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -126,26 +117,35 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else mma_bf16_16816(d, a, b0, b1);
 }
-// Codes as fp16: an integer u < 1024 in the low bits is the subnormal 2^-24 u, exactly.
-// int8 codes, offset to u = c + 128 by kFlip, two bytes of a word at a time; int4
-// codes u = c + 8 from bits 0-3 as 2^-24 u and from bits 4-7, without a shift, as
-// 2^-24 16 u.
+// Codes as 16-bit floats: an integer u < 256 in the low bits is 2^-24 u of fp16 and
+// 2^-133 u of bf16, exactly.  int8 codes, offset to u = c + 128 by kFlip, two bytes of
+// a word at a time; int4 codes u = c + 8 from bits 0-3 as u and from bits 4-7, without a
+// shift, as 16 u.
 constexpr uint32_t kFlip = 0x80808080u;
 constexpr float kUnit = 16777216.f;  // 2^24
 template <int SEL>
-__device__ __forceinline__ uint32_t bytes_f16(uint32_t w) {
+__device__ __forceinline__ uint32_t two_bytes(uint32_t w) {
   return __byte_perm(w, 0u, SEL);  // 5 and 7 pick 0
 }
-__device__ __forceinline__ uint32_t low4_f16(uint32_t w) { return w & 0x000F000Fu; }
-__device__ __forceinline__ uint32_t high4_f16(uint32_t w) { return w & 0x00F000F0u; }
-// The offsets 8 and 128 (of 16 u too), to take off exactly.
-constexpr uint32_t kOff8 = 0x00080008u, kOff128 = 0x00800080u;
-__device__ __forceinline__ uint32_t sub2(uint32_t u, uint32_t off) {
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&off));
-  return *reinterpret_cast<const uint32_t*>(&d);
-}
-// The same negative, as operands.
+__device__ __forceinline__ uint32_t low4(uint32_t w) { return w & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t high4(uint32_t w) { return w & 0x00F000F0u; }
+// The offsets 8 and 128 (of 16 u too), negative, as fp16 operands.
 constexpr uint32_t kLess8 = 0x80088008u, kLess128 = 0x80808080u;
+// bf16 pairs: a b + c.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// Codes 2^-133 u of bf16, times 2^127, less the offset's 2^-6 8 or 2^-6 128.
+constexpr uint32_t kOff8 = 0xBE00BE00u, kOff128 = 0xC000C000u;
+constexpr float kValue = 64.f;  // 2^6
+__device__ __forceinline__ uint32_t centred(uint32_t u, uint32_t off) { return fma_bf16x2(u, 0x7F007F00u, off); }
+// Two values as bf16 pairs: rounded, and what that leaves.
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& high, uint32_t& low) {
+  high = pack_bf16x2(a, b);
+  low = pack_bf16x2(a - __uint_as_float(high << 16), b - __uint_as_float(high & 0xFFFF0000u));
+}
 
 // Layout of a unit's tiles in shared memory and in the fragments.
 template <int KIND, int DIM>
@@ -253,7 +253,8 @@ struct Room {
 
 constexpr int kMaxSeqs = 4096;
 
-// EH: columns of each lane's pair that can be heads; 1: only even columns are.
+// EH: columns of each lane's pair that can be heads; 1: only even columns are, and odd
+// ones take the weights' low parts.
 template <int KIND, int DIM, int NT, int EH, int W, int PER_SM>
 __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_constant__ AttnArgs p) {
   using L = Lay<KIND, DIM>;
@@ -622,8 +623,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
             for (int k = 0; k < L::KW; ++k) {
               x[k] ^= kFlip, y[k] ^= kFlip;
-              const uint32_t a[4] = {bytes_f16<0x5150>(x[k]), bytes_f16<0x5150>(y[k]), bytes_f16<0x5352>(x[k]),
-                                     bytes_f16<0x5352>(y[k])};
+              const uint32_t a[4] = {two_bytes<0x5150>(x[k]), two_bytes<0x5150>(y[k]), two_bytes<0x5352>(x[k]),
+                                     two_bytes<0x5352>(y[k])};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma<true>(s[b][nt], a, qf[nt][2 * (L::KW * i4 + k)], qf[nt][2 * (L::KW * i4 + k) + 1]);
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint32_t xh = h ? x[k] >> 8 : x[k], yh = h ? y[k] >> 8 : y[k];
-                const uint32_t a[4] = {low4_f16(xh), low4_f16(yh), high4_f16(xh), high4_f16(yh)};
+                const uint32_t a[4] = {low4(xh), low4(yh), high4(xh), high4(yh)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma<true>(s[b][nt], a, qf[nt][4 * (L::KW * i4 + k) + 2 * h], qf[nt][4 * (L::KW * i4 + k) + 2 * h + 1]);
@@ -665,14 +666,10 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
               if (16 * b + r1 >= rows) s[b][nt][e + 2] = -INFINITY;
             }
         }
-        // of the weight times its value's scale (at least fp16's smallest)
-        const float g0 = L::QUANT ? fmaxf(log2_(sv[b][0]), -24.f) : 0.f;
-        const float g1 = L::QUANT ? fmaxf(log2_(sv[b][1]), -24.f) : 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < EH; ++e)
-            top[nt][e] = fmaxf(top[nt][e], fmaxf(s[b][nt][e] + g0, s[b][nt][e + 2] + g1));
+          for (int e = 0; e < EH; ++e) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[b][nt][e], s[b][nt][e + 2]));
       }
     }
     // ---- the weights' reference m; what is there is scaled down where it moves -------------
@@ -682,7 +679,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < EH; ++e) above |= top[nt][e] > m[nt][e] + (kUp(L::QUANT) + kSlack(L::QUANT));
+      for (int e = 0; e < EH; ++e) above |= top[nt][e] > m[nt][e] + kSlack;
     if (__any_sync(ALL, above)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -691,7 +688,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         for (int e = 0; e < EH; ++e) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(ALL, top[nt][e], d));
-          const float now = fmaxf(top[nt][e] - kUp(L::QUANT), m[nt][e]);
+          const float now = fmaxf(top[nt][e], m[nt][e]);
           f[e] = m[nt][e] == -INFINITY ? 0.f : exp2_(m[nt][e] - now);
           m[nt][e] = now;
           l[nt][e] *= f[e];
@@ -699,7 +696,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
-          for (int e = 0; e < 4; e += 3 - EH) acc[a][nt][e] *= f[e & 1];
+          for (int e = 0; e < 4; ++e) acc[a][nt][e] *= f[EH == 2 ? e & 1 : 0];
       }
     }
     float ref[NT][2];  // scores of -infinity alone leave m there: their weights are 0
@@ -719,8 +716,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
             if (16 * b + r1 >= rows) f1 = 0.f;
           }
         }
-        uint32_t pb[NT][2];
-        [[maybe_unused]] uint32_t pl[NT][2];
+        uint32_t pb[NT][2], pl[NT][2];  // the weights' parts
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float e[4] = {};
@@ -728,18 +724,23 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
           for (int k = 0; k < 4; k += 3 - EH) e[k] = exp2_(s[b][nt][k] - ref[nt][k & 1]);
           l[nt][0] += e[0] + e[2];
           if (EH == 2) l[nt][1] += e[1] + e[3];
-          if constexpr (L::QUANT) {
-            pb[nt][0] = movmatrix(pack_f16x2(e[0] * f0, e[1] * f0));
-            pb[nt][1] = movmatrix(pack_f16x2(e[2] * f1, e[3] * f1));
-          } else {
-            // two bf16 parts; HBM leaves the time for the second product
-            const uint32_t h0 = pack_bf16x2(e[0], e[1]), h1 = pack_bf16x2(e[2], e[3]);
-            pb[nt][0] = movmatrix(h0);
-            pb[nt][1] = movmatrix(h1);
-            pl[nt][0] = movmatrix(pack_bf16x2(e[0] - __uint_as_float(h0 << 16), e[1] - __uint_as_float(h0 & 0xFFFF0000u)));
-            pl[nt][1] = movmatrix(pack_bf16x2(e[2] - __uint_as_float(h1 << 16), e[3] - __uint_as_float(h1 & 0xFFFF0000u)));
+          if constexpr (L::QUANT) e[0] *= f0, e[1] *= f0, e[2] *= f1, e[3] *= f1;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            split_bf16(e[2 * k], e[2 * k + 1], pb[nt][k], pl[nt][k]);
+            if constexpr (EH == 1) pb[nt][k] |= pl[nt][k] << 16;  // the low part in the odd column
+            else pl[nt][k] = movmatrix(pl[nt][k]);
+            pb[nt][k] = movmatrix(pb[nt][k]);
           }
         }
+        // the values' fragments a into the sums of 16 dims
+        auto add = [&](float (&o)[NT][4], const uint32_t (&a)[4]) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<false>(o[nt], a, pb[nt][0], pb[nt][1]);
+            if (EH == 2) mma<false>(o[nt], a, pl[nt][0], pl[nt][1]);
+          }
+        };
         const uint32_t va = st + L::SIDE + 16 * b * RB;
         const int tk[4] = {L::tok(2 * cl), L::tok(2 * cl + 1), L::tok(2 * cl + 8), L::tok(2 * cl + 9)};
 #pragma unroll
@@ -764,36 +765,26 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
             const int a0 = blk8 * (L::VL / 2) + w * PER;
             if constexpr (KIND == SPEAR_KV_BF16) {
               const uint32_t a[4] = {lo01, hi01, lo89, hi89};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma<false>(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
-                mma<false>(acc[a0][nt], a, pl[nt][0], pl[nt][1]);
-              }
+              add(acc[a0], a);
             } else if constexpr (KIND == SPEAR_KV_INT8) {
               const uint32_t l01 = lo01 ^ kFlip, h01 = hi01 ^ kFlip, l89 = lo89 ^ kFlip, h89 = hi89 ^ kFlip;
-              const uint32_t a[4] = {sub2(bytes_f16<0x5250>(l01), kOff128), sub2(bytes_f16<0x5351>(l01), kOff128),
-                                     sub2(bytes_f16<0x5250>(l89), kOff128), sub2(bytes_f16<0x5351>(l89), kOff128)};
-              const uint32_t c[4] = {sub2(bytes_f16<0x5250>(h01), kOff128), sub2(bytes_f16<0x5351>(h01), kOff128),
-                                     sub2(bytes_f16<0x5250>(h89), kOff128), sub2(bytes_f16<0x5351>(h89), kOff128)};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma<true>(acc[a0][nt], a, pb[nt][0], pb[nt][1]);
-                mma<true>(acc[a0 + 1][nt], c, pb[nt][0], pb[nt][1]);
-              }
+              const uint32_t a[4] = {centred(two_bytes<0x5250>(l01), kOff128), centred(two_bytes<0x5351>(l01), kOff128),
+                                     centred(two_bytes<0x5250>(l89), kOff128), centred(two_bytes<0x5351>(l89), kOff128)};
+              const uint32_t c[4] = {centred(two_bytes<0x5250>(h01), kOff128), centred(two_bytes<0x5351>(h01), kOff128),
+                                     centred(two_bytes<0x5250>(h89), kOff128), centred(two_bytes<0x5351>(h89), kOff128)};
+              add(acc[a0], a);
+              add(acc[a0 + 1], c);
             } else {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint32_t l01 = h ? lo01 >> 8 : lo01, l89 = h ? lo89 >> 8 : lo89;
                 const uint32_t h01 = h ? hi01 >> 8 : hi01, h89 = h ? hi89 >> 8 : hi89;
-                const uint32_t a[4] = {sub2(low4_f16(l01), kOff8), sub2(high4_f16(l01), kOff128),
-                                       sub2(low4_f16(l89), kOff8), sub2(high4_f16(l89), kOff128)};
-                const uint32_t c[4] = {sub2(low4_f16(h01), kOff8), sub2(high4_f16(h01), kOff128),
-                                       sub2(low4_f16(h89), kOff8), sub2(high4_f16(h89), kOff128)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  mma<true>(acc[a0 + h][nt], a, pb[nt][0], pb[nt][1]);
-                  mma<true>(acc[a0 + 2 + h][nt], c, pb[nt][0], pb[nt][1]);
-                }
+                const uint32_t a[4] = {centred(low4(l01), kOff8), centred(high4(l01), kOff128),
+                                       centred(low4(l89), kOff8), centred(high4(l89), kOff128)};
+                const uint32_t c[4] = {centred(low4(h01), kOff8), centred(high4(h01), kOff128),
+                                       centred(low4(h89), kOff8), centred(high4(h89), kOff128)};
+                add(acc[a0 + h], a);
+                add(acc[a0 + 2 + h], c);
               }
             }
           }
@@ -819,6 +810,12 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     // below: lines of code that the stream through L2 has pushed out take long to come.
     fresh = at.j + 1 == at.nt;
     if (fresh || i + 1 == n) {
+      if constexpr (EH == 1) {  // the parts' products
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) acc[a][0][e] += acc[a][0][e + 1];
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -832,7 +829,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
           for (int e = 0; e < EH; ++e) {
             const int h = nt * 8 + 2 * cl + e;
             if (h < gn) {
-              const float even = (L::QUANT ? kUnit : 1.f) / l[nt][e], odd = KIND == SPEAR_KV_INT4 ? 0.0625f * even : even;
+              const float even = (L::QUANT ? kValue : 1.f) / l[nt][e], odd = KIND == SPEAR_KV_INT4 ? 0.0625f * even : even;
               __nv_bfloat16* o = p.out + at.b * p.ld_out + (long long)(h0 + h) * DIM;
 #pragma unroll
               for (int a = 0; a < MT; a += 4) {
@@ -898,7 +895,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
         __stcg(part + 8 * NT * DIM + 8 * NT + h, sum);
       }
     } else {
-      const float inv = (L::QUANT ? kUnit : 1.f) / sum;
+      const float inv = (L::QUANT ? kValue : 1.f) / sum;
       if constexpr (KIND == SPEAR_KV_INT4) o.y *= 0.0625f, o.w *= 0.0625f;  // odd dims, from bits 4-7
       *reinterpret_cast<uint2*>(p.out + pc.b * p.ld_out + (long long)(pc.h0 + h) * DIM + d) =
           make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -1217,8 +1214,9 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
         e = launch_attn<kc.value, dc.value, 2, 2>(a, pl, st);
         return;
       }
-    // One query head per kv head: a lane's second column is none, and its softmax is
-    // left out (int4, 32 x 4099, 32 heads: 63.3 us, 67.0 with it).  bf16 waits for HBM.
+    // One query head per kv head: a lane's second column is none, its softmax is left
+    // out, and the second products too (int4, 32 x 4099, 32 heads: 65.8 us, 69.0 with
+    // the products).  bf16 waits for HBM.
     if constexpr (kc.value != SPEAR_KV_BF16)
       if (a.group == 1) {
         e = launch_attn<kc.value, dc.value, 1, 1>(a, pl, st);
