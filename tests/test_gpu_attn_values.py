@@ -126,3 +126,45 @@ def test_outputs_to_the_precision_of_32_bits(S, kind, dim, group):
     q = bf16_tensor(np.random.default_rng(dim).standard_normal((5, 2 * group, dim)))
     ws = S.make_attn_workspace(f.cache, 2 * group)
     _close(f, q, f64(S.attn_decode(q, f.cache, f.table, f.seq_lens, ws)))
+
+
+INF = float("inf")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 3, 12])
+def test_infinite_values_are_infinite_outputs(S, dim, group):
+    f = Filled(S, "bf16", [1, 2, 33, 700, 4000], 2, dim, 16, seed=dim + group)
+    rng = np.random.default_rng(8)
+    want = {}
+    for b, n in enumerate(f.lens):
+        # a dim each of +, -, both, NaN, and + twice, at tokens of their own
+        for d, what in ((1, (INF,)), (6, (-INF,)), (dim - 3, (INF, -INF)), (dim // 2, (float("nan"),)), (17, (INF, INF))):
+            tokens = rng.permutation(n)[:len(what)]
+            what = what[:len(tokens)]
+            for g in range(2):
+                for t, x in zip(tokens, what):
+                    f.cache.v[f.table[b, t // 16].long(), g, t % 16, d] = x
+                f.v[b][tokens, g, d] = 0.0
+            want[b, d] = sum(what)
+    q = bf16_tensor(rng.standard_normal((5, 2 * group, dim)))
+    ws = S.make_attn_workspace(f.cache, 2 * group)
+    got = f64(S.attn_decode(q, f.cache, f.table, f.seq_lens, ws))
+    for (b, d), x in want.items():
+        assert np.array_equal(got[b, :, d], np.full(2 * group, x), equal_nan=True), (b, d, got[b, :, d])
+        got[b, :, d] = 0.0
+        f.v[b][:, :, d] = 0.0
+    _close(f, q, got)      # the other dims, as if nothing lay beside them
+
+
+def test_an_infinite_value_without_weight_and_behind_the_end(S):
+    # its key is -infinity: 0 times infinity; behind a sequence's end nothing is read
+    f = Filled(S, "bf16", [50, 20], 1, 64, 16, seed=9)
+    f.cache.v[f.table[0, 2].long(), 0, 3, 7] = INF        # token 35
+    f.cache.k[f.table[0, 2].long(), 0, 3, 5] = -INF
+    f.cache.v[f.table[1, 1].long(), 0, 4, 7] = INF        # token 20 of 20
+    q = bf16_tensor(np.random.default_rng(10).standard_normal((2, 2, 64)))
+    q[:, :, 5] = 1.0
+    ws = S.make_attn_workspace(f.cache, 2)
+    got = f64(S.attn_decode(q, f.cache, f.table, f.seq_lens, ws))
+    assert np.all(np.isnan(got[0, :, 7])) and np.isfinite(got).sum() == got.size - 2

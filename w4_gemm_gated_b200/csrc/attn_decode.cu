@@ -141,6 +141,19 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 constexpr uint32_t kOff8 = 0xBE00BE00u, kOff128 = 0xC000C000u;
 constexpr float kValue = 64.f;  // 2^6
 __device__ __forceinline__ uint32_t centred(uint32_t u, uint32_t off) { return fma_bf16x2(u, 0x7F007F00u, off); }
+// Whether one of the 16 bf16 values of these words is infinite or NaN: 0 times it is NaN.
+__device__ __forceinline__ bool any_beyond(const uint32_t (&v)[4][4]) {
+  uint32_t t[2] = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) t[w & 1] = fma_bf16x2(v[k][w], 0u, t[w & 1]);
+  return t[0] | t[1];
+}
+// Two bf16 values, infinities and NaN as 0.
+__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
+  return w & ~__vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
+}
 // Two values as bf16 pairs: rounded, and what that leaves.
 __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& high, uint32_t& low) {
   high = pack_bf16x2(a, b);
@@ -733,12 +746,20 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
             pb[nt][k] = movmatrix(pb[nt][k]);
           }
         }
-        // the values' fragments a into the sums of 16 dims
-        auto add = [&](float (&o)[NT][4], const uint32_t (&a)[4]) {
+        // The values' fragments a into the sums of 16 dims.  An infinite value counts
+        // with the weights' high parts alone: their low parts may be 0 or negative,
+        // and the sum NaN, where the formula's is infinite.
+        auto add = [&](float (&o)[NT][4], const uint32_t (&a)[4], bool beyond = false) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma<false>(o[nt], a, pb[nt][0], pb[nt][1]);
-            if (EH == 2) mma<false>(o[nt], a, pl[nt][0], pl[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt], a, pb[nt][0], pb[nt][1]);
+          if constexpr (EH == 2) {
+            uint32_t r[4] = {a[0], a[1], a[2], a[3]};
+            if (KIND == SPEAR_KV_BF16 && beyond) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) r[k] = finite_part(r[k]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt], r, pl[nt][0], pl[nt][1]);
           }
         };
         const uint32_t va = st + L::SIDE + 16 * b * RB;
@@ -756,6 +777,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
               lds(va + tk[k] * RB + rho * 4, v[k]);
             }
           }
+          bool beyond = false;
+          if constexpr (KIND == SPEAR_KV_BF16) beyond = __any_sync(ALL, any_beyond(v));
 #pragma unroll
           for (int w = 0; w < L::VW; ++w) {
             // the same values of two tokens side by side: low halves, high halves
@@ -765,7 +788,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
             const int a0 = blk8 * (L::VL / 2) + w * PER;
             if constexpr (KIND == SPEAR_KV_BF16) {
               const uint32_t a[4] = {lo01, hi01, lo89, hi89};
-              add(acc[a0], a);
+              add(acc[a0], a, beyond);
             } else if constexpr (KIND == SPEAR_KV_INT8) {
               const uint32_t l01 = lo01 ^ kFlip, h01 = hi01 ^ kFlip, l89 = lo89 ^ kFlip, h89 = hi89 ^ kFlip;
               const uint32_t a[4] = {centred(two_bytes<0x5250>(l01), kOff128), centred(two_bytes<0x5351>(l01), kOff128),
