@@ -68,7 +68,8 @@ uint16_t* bf16_out(const at::Tensor& t) { return static_cast<uint16_t*>(t.data_p
 
 // The device and stream of a call: the current stream of the tensors' device,
 // whichever device is current, or the stream given, which the outputs are then
-// allocated on and whose use of the tensors the allocator is told.
+// allocated on and whose use of the tensors the allocator is told (of the cache's,
+// which come as an address, by the caller).
 struct Where {
   c10::DeviceIndex index;
   std::optional<c10::cuda::CUDAStreamGuard> on;

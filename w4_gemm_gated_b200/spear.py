@@ -433,18 +433,32 @@ def make_kv_cache(kind: int, n_pages: int, page_size: int, n_heads: int, head_di
     return kv_cache_from_parts(k, v, ks, vs)
 
 
+def _used_on(cache: KVCache, stream) -> None:
+    """Tell the allocator that a stream that was given works on the cache's tensors,
+    as the native calls do for their arguments: a cache dropped after the call is
+    not handed out again while the stream's kernels are at it."""
+    for t in (cache.k, cache.v, cache.k_scales, cache.v_scales):
+        if t is not None:
+            t.record_stream(stream)
+
+
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, ws: torch.Tensor,
              stream=None) -> None:
     """Write n new tokens' keys and values (n x n_heads x head_dim or n x (n_heads
     * head_dim) bf16; rows may be ranges of wider rows) at their slots (int32,
     page * page_size + offset; negative: skipped; no slot twice)."""
     _bind.kv_write(cache.address, cache.index, k, v, slots, ws, stream)
+    if stream is not None:
+        _used_on(cache, stream)
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, ws: torch.Tensor, k_out: torch.Tensor | None = None,
             v_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The keys and values at n slots, n x n_heads x head_dim bf16 (a negative slot reads as zeros)."""
-    return _bind.kv_read(cache.address, cache.index, slots, ws, k_out, v_out, stream)
+    out = _bind.kv_read(cache.address, cache.index, slots, ws, k_out, v_out, stream)
+    if stream is not None:
+        _used_on(cache, stream)
+    return out
 
 
 def attn_workspace_bytes(cache: KVCache, n_q_heads: int) -> int:
@@ -473,7 +487,10 @@ def attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_l
     rows may be ranges of wider rows; page_table: n_seqs x max_pages int32;
     seq_lens: int32; scale: 1 / sqrt(head_dim) if None; lse: optional fp32
     n_seqs x n_q_heads, written.  Returns out, of q's shape."""
-    return _bind.attn_decode(cache.address, cache.index, q, page_table, seq_lens, ws, scale, out, lse, stream)
+    out = _bind.attn_decode(cache.address, cache.index, q, page_table, seq_lens, ws, scale, out, lse, stream)
+    if stream is not None:
+        _used_on(cache, stream)
+    return out
 
 
 def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, pre_weight: torch.Tensor | None = None,
