@@ -38,3 +38,18 @@ def test_a_given_stream_is_told_of_the_cache(S, monkeypatch, call, scales):
     log.clear()
     getattr(S, call)(*args, stream="side")
     assert log == ["called"] + [(t, "side") for t in tensors]
+
+
+@pytest.mark.parametrize("linears,attention,first", [(6, 7, 6), (0, 7, 7), (6, 0, 6), (0, 0, 0)])
+def test_status_reads_and_clears_both_workspaces(S, monkeypatch, linears, attention, first):
+    from w4_gemm_gated_b200 import decoder
+    words = {"ws": linears, "attn_ws": attention}
+
+    def read_status(ws):
+        word, words[ws] = words[ws], 0
+        return word
+
+    monkeypatch.setattr(decoder, "S", SimpleNamespace(read_status=read_status))
+    state = SimpleNamespace(ws="ws", attn_ws="attn_ws")
+    assert decoder.status(state) == first
+    assert words == {"ws": 0, "attn_ws": 0} and decoder.status(state) == 0

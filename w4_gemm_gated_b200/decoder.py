@@ -83,5 +83,8 @@ def step(layers: list, x: torch.Tensor, state: StepState, *, norms: list | None 
 
 
 def status(state: StepState) -> int:
-    """The first device-side error of the steps since the last look, of either workspace (synchronises)."""
-    return S.read_status(state.ws) or S.read_status(state.attn_ws)
+    """An error that the device reported in the steps since the last look, 0 if none:
+    the linears' where there is one, else the cache's and the attention's.  Clears
+    both workspaces' words (synchronises)."""
+    of_linears, of_attention = S.read_status(state.ws), S.read_status(state.attn_ws)
+    return of_linears or of_attention
