@@ -53,3 +53,36 @@ def test_status_reads_and_clears_both_workspaces(S, monkeypatch, linears, attent
     state = SimpleNamespace(ws="ws", attn_ws="attn_ws")
     assert decoder.status(state) == first
     assert words == {"ws": 0, "attn_ws": 0} and decoder.status(state) == 0
+
+
+def _attn(S, **kw):
+    """spear_attn_decode with a workspace that is too small: 4 once all else is in order."""
+    import ctypes
+    d = dict(q=0x100000, out=0x200000, ld=4096, seqs=3, table=0x300000, ld_table=6, lens=0x400000, lse=0x500000)
+    d.update(kw)
+    cache = S.KVCacheStruct(kind=1, n_pages=10, page_size=16, n_heads=8, head_dim=128, k=0x1000000, v=0x2000000,
+                            k_scales=0x3000000, v_scales=0x4000000)
+    return S.F["spear_attn_decode"](ctypes.byref(cache), d["q"], d["ld"], d["seqs"], 32, d["table"], 4, d["ld_table"],
+                                    d["lens"], 0.1, d["out"], d["ld"], d["lse"], 0x600000, 255, None)
+
+
+ROWS = 3 * 4096 * 2      # bytes of q and out
+LSE = 3 * 32 * 4
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lse=0x100000), dict(lse=0x100000 + ROWS - 4), dict(lse=0x100000 - LSE + 4),       # q's rows
+    dict(lse=0x200000 + 8192), dict(lse=0x200000 - LSE + 4),                               # out's
+    dict(lse=0x400000), dict(lse=0x400000 + 8), dict(lse=0x300000 + 4 * 15), dict(lse=0x300000 - LSE + 4),
+    dict(lens=0x200000), dict(table=0x200000 + ROWS - 16), dict(table=0x200000 - 4 * 16 + 4),
+])
+def test_attn_refuses_outputs_over_its_inputs(S, kw):
+    assert _attn(S, **kw) == S.ERR_INVALID_ARG and "overlap" in S.F["spear_last_error"]().decode()
+
+
+@pytest.mark.parametrize("kw", [
+    {}, dict(lse=None), dict(lse=0x100000 + ROWS), dict(lse=0x200000 - LSE), dict(lse=0x400000 + 12),
+    dict(lse=0x400000 - LSE), dict(lse=0x300000 + 4 * 16), dict(table=0x200000 + ROWS), dict(lens=0x200000 - 12),
+])
+def test_attn_takes_outputs_beside_its_inputs(S, kw):
+    assert _attn(S, **kw) == S.ERR_WORKSPACE

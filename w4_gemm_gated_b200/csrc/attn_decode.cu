@@ -1200,8 +1200,16 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   for (const void* p : {(const void*)page_table, (const void*)seq_lens, (const void*)lse})
     if (reinterpret_cast<uintptr_t>(p) & 3u)
       return set_error(SPEAR_ERR_ALIGNMENT, "page_table, seq_lens and lse must be 4-byte aligned");
+  const uintptr_t q_bytes = ((n_seqs - 1) * ld_q + row) * 2, out_bytes = ((n_seqs - 1) * ld_out + row) * 2;
+  const uintptr_t table_bytes = ((n_seqs - 1LL) * ld_table + max_pages) * 4, lens_bytes = n_seqs * 4LL;
+  const uintptr_t lse_bytes = (long long)n_seqs * n_q_heads * 4;
+  if (buffers_meet(lse, lse_bytes, q, q_bytes) || buffers_meet(lse, lse_bytes, out, out_bytes))
+    return set_error(SPEAR_ERR_INVALID_ARG, "lse and q or out overlap");
+  if (buffers_meet(lse, lse_bytes, page_table, table_bytes) || buffers_meet(lse, lse_bytes, seq_lens, lens_bytes) ||
+      buffers_meet(out, out_bytes, page_table, table_bytes) || buffers_meet(out, out_bytes, seq_lens, lens_bytes))
+    return set_error(SPEAR_ERR_INVALID_ARG, "an output and page_table or seq_lens overlap");
   // q and out may be column ranges of the same rows, and share nothing else
-  if (buffers_meet(q, ((n_seqs - 1) * ld_q + row) * 2, out, ((n_seqs - 1) * ld_out + row) * 2)) {
+  if (buffers_meet(q, q_bytes, out, out_bytes)) {
     const long long apart = (long long)(reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(q)) / 2;
     const long long column = (apart % ld_q + ld_q) % ld_q;
     if (n_seqs == 1 || ld_q != ld_out || column < row || column + row > ld_q)
