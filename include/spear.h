@@ -296,6 +296,7 @@ int spear_kv_read(const spear_kv_cache* cache, const int* slots, int n, uint16_t
  *            token t of sequence b lies in page page_table[b][t / page_size].
  *            Entries past a sequence's length are not read.
  * seq_lens   device int32 [n_seqs], each 0 to max_pages * page_size.
+ * scale      finite, and its product with log2(e) too (under 2.35e38).
  * lse        optional (NULL): device fp32 [n_seqs][n_q_heads].  It and out are
  *            refused where they overlap q (but for out's columns), one another,
  *            page_table or seq_lens.

@@ -86,3 +86,12 @@ def test_attn_refuses_outputs_over_its_inputs(S, kw):
 ])
 def test_attn_takes_outputs_beside_its_inputs(S, kw):
     assert _attn(S, **kw) == S.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("scale,code", [(2.3e38, 4), (-2.3e38, 4), (2.4e38, 1), (-3.4e38, 1)])
+def test_attn_refuses_a_scale_past_its_range_in_powers_of_two(S, scale, code):
+    # scores are taken in powers of two: scale times log2(e) has to be finite too
+    import ctypes
+    cache = S.KVCacheStruct(kind=0, n_pages=10, page_size=16, n_heads=8, head_dim=128, k=0x1000000, v=0x2000000)
+    assert S.F["spear_attn_decode"](ctypes.byref(cache), 0x100000, 4096, 3, 32, 0x300000, 4, 4, 0x400000, scale, 0x200000,
+                                    4096, None, 0x600000, 255, None) == code

@@ -65,6 +65,7 @@ struct AttnArgs {
 
 constexpr int kRadix = 16;    // parts of a unit joined at once; more are joined in groups of as many first
 constexpr int kMinTiles = 2;  // tiles a warp should have before more CTAs take part
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;  // how far, in powers of two, a weight may lie above 1
 constexpr int kShort = 32;    // tiles up to which a unit stays in one CTA
 
@@ -1184,7 +1185,8 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   if (n_seqs < 0 || n_seqs > kMaxSeqs) return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "n_seqs=%d: must be 0 to 4096", n_seqs);
   if (n_seqs == 0) return SPEAR_OK;
   if (!q || !page_table || !seq_lens || !out || !ws) return set_error(SPEAR_ERR_INVALID_ARG, "NULL pointer");
-  if (!(fabsf(scale) < INFINITY)) return set_error(SPEAR_ERR_INVALID_ARG, "scale=%g: must be finite", scale);
+  if (!(fabsf(scale * kLog2e) < INFINITY))
+    return set_error(SPEAR_ERR_INVALID_ARG, "scale=%g: it and its product with log2(e) must be finite", scale);
   if (max_pages < 1 || ld_table < max_pages)
     return set_error(SPEAR_ERR_INVALID_ARG, "max_pages=%d ld_table=%d: 1 <= max_pages <= ld_table", max_pages, ld_table);
   if ((long long)max_pages * a.c.page_size > 0x7fff0000LL)
@@ -1231,7 +1233,7 @@ extern "C" int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q,
   a.heads = n_q_heads;
   a.group = n_q_heads / a.c.heads;
   a.blocks = pl.blocks;
-  a.scale = scale * 1.4426950408889634f;
+  a.scale = scale * kLog2e;
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.hdr = reinterpret_cast<WsHeader*>(w);
   a.tickets = reinterpret_cast<int*>(w + kWsHeaderBytes);
