@@ -95,3 +95,60 @@ def test_attn_refuses_a_scale_past_its_range_in_powers_of_two(S, scale, code):
     cache = S.KVCacheStruct(kind=0, n_pages=10, page_size=16, n_heads=8, head_dim=128, k=0x1000000, v=0x2000000)
     assert S.F["spear_attn_decode"](ctypes.byref(cache), 0x100000, 4096, 3, 32, 0x300000, 4, 4, 0x400000, scale, 0x200000,
                                     4096, None, 0x600000, 255, None) == code
+
+
+def _child(tmp_path, code):
+    import os
+    import subprocess
+    import sys
+
+    from tests.conftest import ROOT
+    # the package with everything built but the native module
+    pkg = tmp_path / "w4_gemm_gated_b200"
+    pkg.mkdir()
+    src = os.path.join(ROOT, "w4_gemm_gated_b200")
+    for name in os.listdir(src):
+        if not name.startswith("_bind") and name != "__pycache__":
+            os.symlink(os.path.join(src, name), pkg / name)
+    return subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300,
+                          env=dict(os.environ, PYTHONPATH=str(tmp_path)))
+
+
+def test_the_layer_calls_need_no_native_module(S, tmp_path):
+    res = _child(tmp_path, "from w4_gemm_gated_b200 import spear as S, decoder\n"
+                           "assert S.F['spear_device_checks_enabled']() == 0\n"
+                           "print(S.LIB_PATH)")
+    assert res.returncode == 0, res.stderr
+    assert str(tmp_path) in res.stdout
+
+
+@pytest.mark.parametrize("call", ["S.block_norm(None)", "S.kv_read(c, None, None)", "S.kv_write(c, 0, 0, 0, 0)",
+                                  "S.attn_decode(0, c, 0, 0, 0)"])
+def test_the_others_name_the_command_that_builds_it(S, tmp_path, call):
+    res = _child(tmp_path, "from types import SimpleNamespace\nfrom w4_gemm_gated_b200 import spear as S\n"
+                           f"c = SimpleNamespace(address=1, index=0)\ntry:\n    {call}\nexcept ImportError as e:\n    print(e)")
+    assert res.returncode == 0, res.stderr
+    assert "_bind" in res.stdout and "python -m w4_gemm_gated_b200.build" in res.stdout
+
+
+def test_the_native_module_is_rebuilt_for_another_torch(S, monkeypatch, tmp_path):
+    from w4_gemm_gated_b200 import build
+    built = []
+    monkeypatch.setattr(build.subprocess, "run",
+                        lambda cmd, **kw: built.append(cmd) or SimpleNamespace(returncode=0, stdout="", stderr=""))
+    monkeypatch.setattr(build.os, "replace", lambda a, b: None)
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    versions = ["1.0+a"]
+    monkeypatch.setattr(build, "torch_version", lambda: versions[0])
+    build.build_bind()
+    assert len(built) == 1                      # nothing says which torch the one there is of
+    build.build_bind()
+    assert len(built) == 1
+    versions[0] = "1.0+b"
+    build.build_bind()
+    assert len(built) == 2
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **kw: SimpleNamespace(returncode=1, stdout="", stderr="no"))
+    versions[0] = "1.1"
+    for _ in range(2):                          # a build that failed leaves no mark
+        with pytest.raises(RuntimeError):
+            build.build_bind()

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -62,13 +63,21 @@ def _compile(src: str, verbose: bool, checked: bool = False) -> tuple[str, str]:
     return obj, log
 
 
+def torch_version() -> str:
+    return importlib.metadata.version("torch")
+
+
 def build_bind(force: bool = False) -> str:
     """The binding's native module; its CUDA side is reached through addresses
-    handed to it, so it links to torch alone."""
+    handed to it, so it links to torch alone: to the C++ of one version, which
+    a file in the objects' folder names."""
     src, header = os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "spear.h")
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(os.path.getmtime(src),
-                                                                           os.path.getmtime(header)):
-        return BIND
+    mark, version = os.path.join(BUILD, "bind.torch"), torch_version()
+    if not force and os.path.exists(BIND) and os.path.exists(mark):
+        with open(mark) as f:
+            built_for = f.read()
+        if built_for == version and os.path.getmtime(BIND) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+            return BIND
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -84,6 +93,9 @@ def build_bind(force: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for bind.cpp:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BIND)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(mark, "w") as f:
+        f.write(version)
     return BIND
 
 

@@ -1,9 +1,11 @@
-"""ctypes binding of ``libspear.so`` (C ABI in ``include/spear.h``).
+"""Binding of ``libspear.so`` (C ABI in ``include/spear.h``): ctypes, and for the
+cache, attention and norm calls the native module ``_bind``.
 
 Argument marshalling only: every step of the layer runs in the CUDA library.
 PyTorch tensors supply device memory and the current CUDA stream.  Importing
 this module loads the library and raises ``ImportError`` if it is missing;
-there is no fallback implementation.
+without the native module the calls that it marshals raise it.  There is no
+fallback implementation.
 """
 from __future__ import annotations
 
@@ -21,7 +23,23 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), _LIB_NAME)
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with `python -m w4_gemm_gated_b200.build`")
 _lib = ctypes.CDLL(_LIB_PATH)
-from . import _bind  # noqa: E402  (native marshalling of the decoder-step calls, built beside the library)
+
+
+class _NoBind:
+    """In the place of the native module where it is missing or does not load."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the native module _bind of {name} is missing or does not load ({self._why}): build it with "
+                          "`python -m w4_gemm_gated_b200.build`")
+
+
+try:
+    from . import _bind  # native marshalling of the decoder-step calls, built beside the library
+except ImportError as e:
+    _bind = _NoBind(e)
 
 OK = 0
 ERR_INVALID_ARG = 1
@@ -508,8 +526,9 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, pre_weight: to
                             stream)
 
 
-_bind.setup(*(ctypes.cast(F[name], _vp).value for name in ("spear_kv_write", "spear_kv_read", "spear_attn_decode",
-                                                           "spear_block_norm")), _check)
+if not isinstance(_bind, _NoBind):
+    _bind.setup(*(ctypes.cast(F[name], _vp).value for name in ("spear_kv_write", "spear_kv_read", "spear_attn_decode",
+                                                               "spear_block_norm")), _check)
 
 
 def test_inject_timeout(kernel: int, wait_cycles: int = 0) -> None:
