@@ -269,6 +269,8 @@ size_t spear_kv_page_scales(int kind, int page_size, int n_heads, int head_dim);
  * slots   device int32 [n].  A negative slot skips its token (padding).  The
  *         others must differ from one another: a slot given twice in a call
  *         ends with an unspecified mixture of its tokens.
+ * cache   k, v and the scales must not overlap (one array may stand for keys and
+ *         values where a cache is only read): refused where it shows.
  * ws      device, 256 bytes or more, as of spear_workspace_init: a slot past
  *         the cache's end is skipped and reported there as
  *         SPEAR_ERR_DEVICE_CHECK (spear_read_status).

@@ -152,3 +152,40 @@ def test_the_native_module_is_rebuilt_for_another_torch(S, monkeypatch, tmp_path
     for _ in range(2):                          # a build that failed leaves no mark
         with pytest.raises(RuntimeError):
             build.build_bind()
+
+
+PAGE = 8 * 16 * 128          # bytes of a page of int8 keys
+PAGE_SCALES = 8 * 16 * 2
+
+
+def _write(S, **kw):
+    """spear_kv_write of too many tokens: unsupported (2) once the cache is in order."""
+    import ctypes
+    d = dict(kind=1, n_pages=10, page_size=16, n_heads=8, head_dim=128, k=0x1000000, v=0x2000000, k_scales=0x3000000,
+             v_scales=0x4000000)
+    d.update(kw)
+    return S.F["spear_kv_write"](ctypes.byref(S.KVCacheStruct(**d)), 0x100000, 1024, 0x200000, 1024, 0x300000,
+                                 2147483647, 0x400000, 256, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(v=0x1000000), dict(v=0x1000000 + 16), dict(v=0x1000000 + 10 * PAGE - 16), dict(v=0x1000000 - 10 * PAGE + 16),
+    dict(v=0x1000000, n_pages=1), dict(k_scales=0x4000000), dict(v_scales=0x3000000 + PAGE_SCALES),
+    dict(page_stride=2 * PAGE, v=0x1000000 + PAGE - 16), dict(page_stride=2 * PAGE, v=0x1000000 + PAGE + 16),
+    dict(page_stride=2 * PAGE - 16, v=0x1000000 + PAGE), dict(page_stride=2 * PAGE, v=0x1000000 + 4 * PAGE),
+    dict(kind=0, k_scales=None, v_scales=None, v=0x1000000 + 2 * PAGE),
+    # scales in the pages' rows: of the keys over the values
+    dict(page_stride=4 * PAGE, scale_stride=2 * PAGE, v=0x1000000 + PAGE, k_scales=0x1000000 + 2 * PAGE - 16),
+])
+def test_kv_write_refuses_a_cache_whose_parts_overlap(S, kw):
+    assert _write(S, **kw) == S.ERR_INVALID_ARG and "overlap" in S.F["spear_last_error"]().decode()
+
+
+@pytest.mark.parametrize("kw", [
+    {}, dict(v=0x1000000 + 10 * PAGE), dict(v=0x1000000 - 10 * PAGE), dict(page_stride=2 * PAGE, v=0x1000000 + PAGE),
+    dict(page_stride=2 * PAGE, v=0x1000000 - PAGE), dict(page_stride=2 * PAGE, v=0x1000000 + 5 * PAGE),
+    dict(page_stride=4 * PAGE, scale_stride=2 * PAGE, v=0x1000000 + PAGE, k_scales=0x1000000 + 2 * PAGE,
+         v_scales=0x1000000 + 2 * PAGE + PAGE_SCALES),
+])
+def test_kv_write_takes_parts_beside_one_another(S, kw):
+    assert _write(S, **kw) == S.ERR_UNSUPPORTED_SHAPE, S.F["spear_last_error"]().decode()

@@ -313,6 +313,31 @@ static int check_tokens(const int* slots, int n, const void* ws, size_t ws_bytes
   return SPEAR_OK;
 }
 
+// Whether two of a cache's arrays of pages share bytes.  Those whose pages lie as far
+// apart may lie beside one another in larger pages; of others nothing is said where
+// their ranges meet.
+static bool pages_meet(const void* a, long long step_a, long long bytes_a, const void* b, long long step_b,
+                       long long bytes_b, int n_pages) {
+  if (!buffers_meet(a, (n_pages - 1) * step_a + bytes_a, b, (n_pages - 1) * step_b + bytes_b)) return false;
+  if (n_pages == 1) return true;
+  if (step_a != step_b) return false;
+  const long long apart = (long long)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  const long long column = (apart % step_a + step_a) % step_a;
+  return column < bytes_a || column + bytes_b > step_a;
+}
+
+static bool parts_meet(const KvView& c) {
+  const long long codes = (long long)c.heads * c.dim * kv_bits(c.kind) / 8 << c.log_page;
+  const long long scales = (long long)c.heads * 2 << c.log_page;
+  const void* part[4] = {c.k, c.v, c.ks, c.vs};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j)
+      if (pages_meet(part[i], i < 2 ? c.page_stride : c.scale_stride * 2, i < 2 ? codes : scales, part[j],
+                     j < 2 ? c.page_stride : c.scale_stride * 2, j < 2 ? codes : scales, c.n_pages))
+        return true;
+  return false;
+}
+
 static int blocks_for(long long rows, int dim, int step) {
   const int per = step * kThreads / (dim / 16);
   return (int)((rows + per - 1) / per);
@@ -355,6 +380,7 @@ extern "C" int spear_kv_write(const spear_kv_cache* cache, const uint16_t* k, lo
   const long long row = (long long)c.heads * c.dim;
   if (ld_k < row || ld_v < row || ld_k % 8 || ld_v % 8)
     return set_error(SPEAR_ERR_INVALID_ARG, "ld_k=%lld ld_v=%lld: multiples of 8 of at least %lld", ld_k, ld_v, row);
+  if (parts_meet(c)) return set_error(SPEAR_ERR_INVALID_ARG, "the cache's k, v and scales overlap");
   if ((long long)n * c.heads > (1LL << 31)) return set_error(SPEAR_ERR_UNSUPPORTED_SHAPE, "n=%d: too many rows", n);
   const unsigned rows = (unsigned)n * c.heads;
   const int step = step_for(rows, c.dim);
