@@ -357,7 +357,9 @@ int spear_test_inject_timeout(int kernel, long long wait_cycles);
  * The library can be built a second time with -DSPEAR_DEVICE_CHECKS
  * (libspear_checked.so beside libspear.so): device-side bounds checks on the
  * kernels' output stores (row < M, channels < N) and on their workspace
- * partial slots, flags and published EC rows.  A failed check writes
+ * partial slots, flags and published EC rows; on the attention's outputs
+ * (sequence, head), parts and counters, and the cache calls' rows.  The norm
+ * call has no status word and no such checks.  A failed check writes
  * SPEAR_ERR_DEVICE_CHECK to the status word (spear_read_status), skips the
  * access it guards and never traps; y is then unspecified.  In the normal
  * build the checks compile away.

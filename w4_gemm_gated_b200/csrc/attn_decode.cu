@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   const uint32_t ring_end = ring_a + R::RING;
   auto issue = [&]() {
     if (done < n) {
-      copy_tile(put);
+      if (SPEAR_DCHECK(put >= ring_a && put + L::STAGE <= ring_end, p.hdr)) copy_tile(put);
       put = put + L::STAGE == ring_end ? ring_a : put + L::STAGE;
       advance<TILE>(p, in);
     }
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < EH; ++e) {
             const int h = nt * 8 + 2 * cl + e;
-            if (h < gn) {
+            if (h < gn && SPEAR_DCHECK(at.b < p.n_seqs && h0 + h < p.heads, p.hdr)) {
               const float even = (L::QUANT ? kValue : 1.f) / l[nt][e], odd = KIND == SPEAR_KV_INT4 ? 0.0625f * even : even;
               __nv_bfloat16* o = p.out + at.b * p.ld_out + (long long)(h0 + h) * DIM;
 #pragma unroll
@@ -913,12 +913,13 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
     const int h = item / CH, d = (item % CH) * 128 + 4 * lane;
     if (4 * lane >= LD) return;
     if (part) {
+      if (!SPEAR_DCHECK(part >= p.parts && part + R::PIECE <= p.parts + (size_t)p.ctas * 2 * R::PIECE, p.hdr)) return;
       __stcg(reinterpret_cast<float4*>(part + h * DIM + d), o);
       if (d == 0) {
         __stcg(part + 8 * NT * DIM + h, mx);
         __stcg(part + 8 * NT * DIM + 8 * NT + h, sum);
       }
-    } else {
+    } else if (SPEAR_DCHECK(pc.b < p.n_seqs && pc.h0 + h < p.heads, p.hdr)) {
       const float inv = (L::QUANT ? kValue : 1.f) / sum;
       if constexpr (KIND == SPEAR_KV_INT4) o.y *= 0.0625f, o.w *= 0.0625f;  // odd dims, from bits 4-7
       *reinterpret_cast<uint2*>(p.out + pc.b * p.ld_out + (long long)(pc.h0 + h) * DIM + d) =
@@ -1065,6 +1066,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
       // a unit's last CTA may be the first of another's: each counts on its part's side
       ticket = p.tickets + p.ctas + 2 * job.first + (job.first == job.c0);
     }
+    if (!SPEAR_DCHECK(job.c0 >= 0 && job.c0 + count <= (int)ctas, p.hdr)) ticket = nullptr;
   }
 #pragma unroll 1
   for (bool more = true; more;) {

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
 #pragma unroll
   for (int u = 0; u < STEP; ++u) {
     const int page = slot[u] >> c.log_page;
-    const bool live = slot[u] >= 0 && page < c.n_pages;
+    const bool live = slot[u] >= 0 && page < c.n_pages && SPEAR_DCHECK(head[u] < (unsigned)c.heads, hdr);
     if (slot[u] >= 0 && !live && lane_r == 0) report_status(hdr, SPEAR_ERR_DEVICE_CHECK);
     const int prow = (head[u] << c.log_page) + (slot[u] & (c.page_size - 1));  // row inside the page
     uint8_t* dst = (is_v ? c.v : c.k) + (page_at(live ? page : 0, c.page_step) << 4) +
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
       split_row(row0 + r, c.heads, magic, tok, head);
       const int slot = slots[tok];
       const int page = slot >> c.log_page;
-      live[u] = slot >= 0 && page < c.n_pages;
+      live[u] = slot >= 0 && page < c.n_pages && SPEAR_DCHECK(head < (unsigned)c.heads, hdr);
       if (live[u]) {
         const int prow = (head << c.log_page) + (slot & (c.page_size - 1));
         const uint8_t* src = codes + (page_at(page, c.page_step) << 4) + (long long)prow * (DIM / 8 * BYTES);
