@@ -247,8 +247,8 @@ typedef struct spear_kv_cache {
   void* k;        /* device, [n_pages][n_heads][page_size][head_dim]: bf16; int8 codes */
   void* v;        /*   (two's complement); or int4 codes, byte j of a row holding      */
                   /*   (c[2j] + 8) | (c[2j+1] + 8) << 4                                */
-  uint16_t* k_scales; /* device fp16, [n_pages][n_heads][page_size] (NULL for bf16)    */
-  uint16_t* v_scales;
+  uint16_t* k_scales; /* device fp16, [n_pages][n_heads][page_size] (NULL for bf16),   */
+  uint16_t* v_scales; /*   of cached tokens finite, or NaN for a row that holds one     */
   /* Distance of consecutive pages, for pages that lie inside a larger
    * allocation (K and V of a page side by side, pages of several layers):
    * bytes for k and v, elements for the scales.  Multiples of 16 bytes, at
@@ -266,6 +266,7 @@ size_t spear_kv_page_scales(int kind, int page_size, int n_heads, int head_dim);
  * k, v    device bf16, n rows of n_heads * head_dim; ld_k, ld_v: elements
  *         between consecutive rows (a multiple of 8; at least a row), so that
  *         column ranges of one projection's output can be passed as they are.
+ *         They must not lie in the cache's own pages.
  * slots   device int32 [n].  A negative slot skips its token (padding).  The
  *         others must differ from one another: a slot given twice in a call
  *         ends with an unspecified mixture of its tokens.
@@ -279,7 +280,7 @@ int spear_kv_write(const spear_kv_cache* cache, const uint16_t* k, long long ld_
                    const int* slots, int n, void* ws, size_t ws_bytes, void* stream);
 
 /* Read n tokens back: k_out, v_out device bf16 [n][n_heads][head_dim] (dense, apart
- * from one another), bf16_rne(c * s).  Slots may repeat; a negative slot's rows are zeros, and so
+ * from one another and from the cache), bf16_rne(c * s).  Slots may repeat; a negative slot's rows are zeros, and so
  * are those of a slot past the cache's end, which is reported as above. */
 int spear_kv_read(const spear_kv_cache* cache, const int* slots, int n, uint16_t* k_out, uint16_t* v_out, void* ws,
                   size_t ws_bytes, void* stream);
@@ -312,7 +313,13 @@ int spear_kv_read(const spear_kv_cache* cache, const int* slots, int n, uint16_t
  * SPEAR_ERR_DEVICE_CHECK (spear_read_status), and the sequence's results are
  * then unspecified.  0 <= n_seqs <= 4096 (0: nothing is launched);
  * n_seqs * max_pages * page_size * n_q_heads < 2^35.  The result does not depend on
- * timing: the split over the cache is a function of the sizes and lengths alone. */
+ * timing: the split over the cache is a function of the sizes and lengths alone.
+ * The table's room (n_seqs * max_pages * page_size) is one of these sizes: where
+ * more than 8 query heads share a kv head it selects between two forms of the
+ * kernel, whose outputs may differ in their last bit and whose times do (a table
+ * no wider than the batch needs is the faster one for short sequences).
+ * Sums are held in 32 bits, with weights of up to 2^8: values so large that
+ * 2^8 sum_t |v_t| passes 3.4e38 may give an infinite output. */
 size_t spear_attn_workspace_bytes(const spear_kv_cache* cache, int n_q_heads);
 int spear_attn_decode(const spear_kv_cache* cache, const uint16_t* q, long long ld_q, int n_seqs, int n_q_heads,
                       const int* page_table, int max_pages, int ld_table, const int* seq_lens, float scale,

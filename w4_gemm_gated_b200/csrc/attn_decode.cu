@@ -2,9 +2,9 @@
 //
 //   out_h = sum_t p_t v_t,  p = softmax(scale q_h . k_t)
 //
-// Each cached byte is read once and used for the few query heads that share it (two
+// Each cached byte is read once for every 8 or 16 of the query heads that share it (two
 // operations per value and head), so HBM bounds it in principle, and does for
-// bf16: 2 sequences of up to 131,072 tokens, 8 heads of 128, 800 MB in 128 us, 6.2
+// bf16 and groups of up to 8: 2 sequences of up to 131,072 tokens, 8 heads of 128, 800 MB in 128 us, 6.2
 // TB/s.  Quantised caches take a few instructions per code, which bound them where
 // no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 66 us, 4.1 TB/s).  Short batches are bound by the chain from the lengths over
 // the page table to the data and by the joins (int8, 16 x 2048: 36 MB in 17 us).
@@ -242,8 +242,8 @@ struct Cut {
 // Warps of a CTA and CTAs of an SM.  Two CTAs, so that one streams while the other
 // starts or joins (bf16, 64 x 4096: one of 8 warps 108 us, two of 4 101, four of 2
 // 103).  Quantised kinds are bound by their arithmetic and take 16 warps where 128
-// registers do (two of 8; with two of 4 int8 of 16 x 2048 takes 18.1 us, not 17.0, and
-// int4 of 32 x 4099 with 32 heads 7 % more).
+// registers do (two of 8; with two of 4 int8 of 16 x 2048 takes 17.2 us, not 16.1, and
+// int4 of 32 x 4099 with 32 heads 11 % more).
 constexpr bool attn_small(int kind, int dim, int nt) { return kind != SPEAR_KV_BF16 && dim < 256 && nt == 1; }
 constexpr int attn_warps(int kind, int dim, int nt) { return attn_small(kind, dim, nt) ? 8 : 4; }
 constexpr int attn_per_sm(int kind, int dim) {  // at most 2, which the workspace counts on
@@ -367,8 +367,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   // Where no unit is longer than kShort tiles, CTAs take whole units: the borders
   // of even runs move on to the next unit's start.  A CTA may then have up to
   // kShort tiles more than its share, which costs no more than joining a unit
-  // across CTAs does and saves that (7 sequences to 1001 tokens, 2 heads of 64: 9.0 us,
-  // 10.7 with joins; a single sequence of 97, 8 heads, pays for it: 5.9 us, 5.4).
+  // across CTAs does and saves that (7 sequences to 1001 tokens, 2 heads of 64: 9.9 us,
+  // 11.2 with joins; a single sequence of 97, 8 heads, pays for it: 6.6 us, 6.2).
   const bool aligned = longest <= kShort;
   const unsigned ctas = min(gridDim.x, aligned ? min(total, (unsigned)(p.n_seqs * units))
                                                : (total + kMinTiles * W - 1) / (kMinTiles * W));
@@ -604,7 +604,8 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
   auto work = [&](const uint32_t st, const int rows, auto whole) {
     constexpr bool WHOLE = decltype(whole)::value;
     // ---- scores: S[token][head] --------------------------------------------------------
-    float s[TS][NT][4], sv[TS][2];  // scores; the values' scales of this lane's two tokens
+    float s[TS][NT][4];  // scores
+    [[maybe_unused]] float sv[TS][2];  // the values' scales of this lane's two tokens
     float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(W * 32, PER_SM) attn_kernel(const __grid_const
               lds(va + tk[k] * RB + rho * 4, v[k]);
             }
           }
-          bool beyond = false;
+          [[maybe_unused]] bool beyond = false;
           if constexpr (KIND == SPEAR_KV_BF16) beyond = __any_sync(ALL, any_beyond(v));
 #pragma unroll
           for (int w = 0; w < L::VW; ++w) {
@@ -1114,8 +1115,14 @@ struct AttnPlan {
 // tokens: of all sequences, at most.  Groups of more than 8 query heads go through
 // two products side by side, which read a tile once, where there are tiles enough;
 // else as units of 8 each, of which twice as many warps run and join smaller parts
-// (heads 48/4 of 128, sequences to 4096; int8: 64 of them 53.7 us, 64.5 as units of
-// 8, 16 of them 24.5, 22.2; bf16: 62.1, 88.5, and 27.8, 26.2; 8 of them 23.3, 18.7).
+// (heads 48/4 of 128, sequences to 4096; int8: 64 of them 55.9 us, 65.4 as units of
+// 8, 32 of them 37.3, 39.4, 16 of them 24.6, 22.0; bf16: 64 of them 63.2, 88.8, 16 of
+// them 27.5, 26.6, 8 of them 23.5, 19.3; int4: 47.6, 58.0, and 23.3, 20.4).  The host does
+// not know the lengths, so the table's room counts: short sequences under a wide
+// table get the form that is slower for them (int8, 16 of up to 512 tokens: 16.5 us
+// under a table for 65,536, 12.0 under one for 512).  256-wide heads have no
+// registers for two products: their groups past 8 always read the cache again (bf16,
+// 8 of up to 32,768, 2 kv heads: 55.5 us with 8 heads each, 77.5 with 16).
 static AttnPlan plan_attn(const KvView& c, int n_q_heads, long long tokens) {
   AttnPlan a;
   const int group = n_q_heads / c.heads;

@@ -504,7 +504,9 @@ def attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_l
     q: n_seqs x n_q_heads x head_dim or n_seqs x (n_q_heads * head_dim) bf16,
     rows may be ranges of wider rows; page_table: n_seqs x max_pages int32;
     seq_lens: int32; scale: 1 / sqrt(head_dim) if None; lse: optional fp32
-    n_seqs x n_q_heads, written.  Returns out, of q's shape."""
+    n_seqs x n_q_heads, written.  Returns out, of q's shape.  A page_table no
+    wider than the batch needs is the faster one for short sequences where more
+    than 8 query heads share a kv head."""
     out = _bind.attn_decode(cache.address, cache.index, q, page_table, seq_lens, ws, scale, out, lse, stream)
     if stream is not None:
         _used_on(cache, stream)
