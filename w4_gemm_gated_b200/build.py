@@ -64,7 +64,11 @@ def _compile(src: str, verbose: bool, checked: bool = False) -> tuple[str, str]:
 
 
 def torch_version() -> str:
-    return importlib.metadata.version("torch")
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # not installed as a package
+        import torch
+        return str(torch.__version__)
 
 
 def build_bind(force: bool = False) -> str:

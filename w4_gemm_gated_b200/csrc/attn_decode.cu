@@ -2,12 +2,14 @@
 //
 //   out_h = sum_t p_t v_t,  p = softmax(scale q_h . k_t)
 //
-// Each cached byte is read once for every 8 or 16 of the query heads that share it (two
-// operations per value and head), so HBM bounds it in principle, and does for
-// bf16 and groups of up to 8: 2 sequences of up to 131,072 tokens, 8 heads of 128, 800 MB in 128 us, 6.2
-// TB/s.  Quantised caches take a few instructions per code, which bound them where
-// no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 66 us, 4.1 TB/s).  Short batches are bound by the chain from the lengths over
-// the page table to the data and by the joins (int8, 16 x 2048: 36 MB in 17 us).
+// Each cached byte is read once for every 8 or 16 of the query heads that share it
+// (two operations per value and head), so HBM bounds it in principle, and does for
+// bf16 and groups of up to 8: 2 sequences of up to 131,072 tokens, 8 heads of 128,
+// 800 MB in 128 us, 6.2 TB/s.  Quantised caches take a few instructions per code,
+// which bound them where no heads share them (int4, 32 x 4099, 32 heads: 272 MB in 66
+// us, 4.1 TB/s, at 58 % of the issue rate).  Short batches are bound by the chain from
+// the lengths over the page table to the data and by the joins (int8, 16 x 2048: 36
+// MB in 17 us).
 //
 // Work.  A unit is one (sequence, kv head) with up to 8 NT query heads; its
 // tokens are cut into tiles of TILE.  All units' tiles in order form one line
