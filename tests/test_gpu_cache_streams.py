@@ -1,4 +1,5 @@
-"""Caches that are dropped while another stream still works on them."""
+"""Caches that are dropped while another stream still works on them, and caches
+whose parts share an allocation."""
 import numpy as np
 import pytest
 import torch
@@ -70,3 +71,54 @@ def test_a_write_on_a_stream_reaches_no_later_tensor(S, kind):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert all(torch.all(t.view(torch.uint8) == 0x5A) for t in made)
+
+
+# ---- caches whose parts share an allocation ---------------------------------------------------
+@pytest.mark.parametrize("kind", ["bf16", "int8", "int4"])
+def test_keys_and_values_of_a_page_side_by_side(S, kind):
+    f = Filled(S, kind, [200, 33], 2, 64, 16, seed=5)
+    c = f.cache
+    pages = torch.stack([c.k, c.v], dim=1)                    # n_pages x 2 x heads x page x dim
+    scales = None if kind == "bf16" else torch.stack([c.k_scales, c.v_scales], dim=1)
+    f.cache = S.kv_cache_from_parts(pages[:, 0], pages[:, 1], *(() if scales is None else (scales[:, 0], scales[:, 1])))
+    ws = S.make_attn_workspace(f.cache, 4)
+    q = bf16_tensor(np.random.default_rng(6).standard_normal((2, 4, 64)))
+    f.check(S, q, S.attn_decode(q, f.cache, f.table, f.seq_lens, ws), None, 0.125, ws)
+    k, v = (bf16_tensor(np.random.default_rng(i).standard_normal((40, 2, 64))) for i in (7, 8))
+    slots = (f.table[0, :3].long()[:, None] * 16 + torch.arange(16, device="cuda")).flatten()[:40].to(torch.int32)
+    S.kv_write(f.cache, k, v, slots, ws)
+    got = S.kv_read(f.cache, slots, ws)
+    S.kv_write(c, k, v, slots, ws)                            # the same into pages apart
+    assert all(torch.equal(a, b) for a, b in zip(got, S.kv_read(c, slots, ws)))
+    bits = [t.contiguous().view(torch.uint8) for t in (pages[:, 0], c.k, pages[:, 1], c.v)]   # free places hold NaN
+    assert torch.equal(bits[0], bits[1]) and torch.equal(bits[2], bits[3]) and S.read_status(ws) == S.OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "int4"])
+def test_one_array_for_keys_and_values_is_read_and_not_written(S, kind):
+    f = Filled(S, kind, [90, 20], 2, 64, 16, seed=9)
+    c = f.cache
+    f.cache = S.kv_cache_from_parts(c.k, c.k, c.k_scales, c.k_scales)
+    f.v = f.k
+    ws = S.make_attn_workspace(f.cache, 4)
+    q = bf16_tensor(np.random.default_rng(10).standard_normal((2, 4, 64)))
+    f.check(S, q, S.attn_decode(q, f.cache, f.table, f.seq_lens, ws), None, 0.125, ws)
+    k = bf16_tensor(np.random.default_rng(11).standard_normal((2, 2, 64)))
+    with pytest.raises(S.SpearError):
+        S.kv_write(f.cache, k, k, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), ws)
+
+
+def test_calls_on_a_given_stream_are_captured(S):
+    f = Filled(S, "int8", [700, 33], 2, 64, 16, seed=12)
+    ws = S.make_attn_workspace(f.cache, 4)
+    q = bf16_tensor(np.random.default_rng(13).standard_normal((2, 4, 64)))
+    want = S.attn_decode(q, f.cache, f.table, f.seq_lens, ws)
+    out, side, graph = torch.zeros_like(want), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        S.attn_decode(q, f.cache, f.table, f.seq_lens, ws, out=out, stream=side)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
